@@ -965,3 +965,19 @@ class EPMoELayer:
         dist.barrier(group=self.group)
         peer_free(self._base)
         self._closed = True
+
+
+# The handle-free expert-layer operators (operators.py) are part of the package's
+# surface; they are loaded on first use, as they need torch to be imported.
+OPERATORS = ("route", "route_backward", "group_rows", "quantize_rows_fp8", "quantize_weights_fp8",
+             "glu_quantize_fp8", "glu_backward_quantize_fp8", "matmul_fp8", "combine_rows",
+             "combine_rows_backward", "operator_error")
+
+
+def __getattr__(name):
+    if name in OPERATORS:
+        from . import operators
+        value = getattr(operators, name)
+        globals()[name] = value
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,587 @@
+// Routing to experts from given logits, its gradient, and the grouping of the
+// chosen (token, slot) rows by expert.
+//
+//   s    = softmax(l) or sigmoid(l)                     scores, all E experts
+//   key  = s + b                                        b selects only (balance)
+//   score of a group = the sum of its group_top (1 or 2) largest keys; the
+//   topk_groups best groups stay; the k largest keys in them are chosen, ties to
+//   the lower index; w_j = scale * s_j [/ sum_i s_i over the chosen].
+// (nxmr.cn "V4" article, §2.2; DeepSeek V4 infra notes, §6.3; the linux.do post on
+// MoE variants, "QuantileBalancing".)
+//
+// Selection follows the keys' order in exact arithmetic.  Without a bias the
+// scores grow with the logits, so the logits themselves are the keys and every
+// comparison is exact.  With one, keys are formed in fp32 and two neighbours in
+// the order that lie within the error bound below send the row to a second pass
+// in fp64 (about two rows in a thousand of normal logits).
+#include <cfloat>
+
+#include "common.cuh"
+#include "moe_internal.h"
+#include "ops_internal.h"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+
+// fp32 as an unsigned integer of the same order; 0 is below every number (it
+// stands for "cannot be chosen").  -0 and +0 are one value.
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ uint32_t key_of(float v) {
+  // NaN and -inf can never be chosen.
+  return v > -INFINITY ? order_of(v) : 0u;
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+__device__ __forceinline__ float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// How far two fp32 keys of about this size can be from their exact difference.
+// sigmoid: expf 2 ulp, the sum and the division half an ulp each: below 1.8e-7 for
+// s <= 1; softmax: the argument's rounding and the fp32 sum of up to 1024 terms
+// add about 4e-7 s; the sum with the bias 2^-24 |key|.  Doubled for two keys.
+__device__ __forceinline__ float close_bound(float key) { return 1.2e-6f + 2.5e-7f * fabsf(key); }
+
+// The whole row again in fp64, for rows whose fp32 keys are too close to order.
+// Returns the expert of slot `lane` (-1: none).
+template <int CPL, typename In>
+__device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, int lane, int first, int count) {
+  const double ninf = -static_cast<double>(INFINITY);
+  double key[CPL];
+  double m = ninf;
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) {
+    key[i] = ninf;
+    if (i < count) {
+      const double l = static_cast<double>(to_float(row[first + i]));
+      if (l > ninf) { key[i] = l; m = fmax(m, l); }
+    }
+  }
+  if (a.softmax) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (key[i] > ninf) { key[i] = exp(key[i] - m); sum += key[i]; }
+      else key[i] = ninf;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (key[i] > ninf) key[i] /= sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (key[i] > ninf) key[i] = 1.0 / (1.0 + exp(-key[i]));
+  }
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (key[i] > ninf) {
+        key[i] += static_cast<double>(a.bias[first + i]);
+        if (!(key[i] > ninf)) key[i] = ninf;
+      }
+  }
+  if (a.topk_groups < a.n_groups) {
+    double m1 = ninf, m2 = ninf;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      if (key[i] > m1) { m2 = m1; m1 = key[i]; }
+      else if (key[i] > m2) m2 = key[i];
+    }
+    for (int o = 1; o < a.lpg; o <<= 1) {
+      const double o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+      const double hi = fmax(m1, o1), lo = fmin(m1, o1);
+      m2 = fmax(lo, fmax(m2, o2));
+      m1 = hi;
+    }
+    // A group with one expert left scores by that one.
+    const double score = (a.group_top == 2 && m2 > ninf) ? m1 + m2 : m1;
+    const int g = lane / a.lpg;
+    int rank = 0;
+    for (int q = 0; q < a.n_groups; ++q) {
+      const double sq = __shfl_sync(kFull, score, q * a.lpg);
+      if (sq > score || (sq == score && q < g)) ++rank;
+    }
+    if (rank >= a.topk_groups)
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) key[i] = ninf;
+  }
+  int chosen = -1;
+  for (int j = 0; j < a.k; ++j) {
+    double bk = ninf;
+    int be = 0x7fffffff;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (key[i] > bk) { bk = key[i]; be = first + i; }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ok = __shfl_xor_sync(kFull, bk, o);
+      const int oe = __shfl_xor_sync(kFull, be, o);
+      if (ok > bk || (ok == bk && oe < be)) { bk = ok; be = oe; }
+    }
+    if (!(bk > ninf)) break;
+    if (lane == j) chosen = be;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (first + i == be) key[i] = ninf;
+  }
+  return chosen;
+}
+
+// One warp per token.  Lane l owns cpl consecutive experts of group l / lpg, so
+// lanes hold experts in index order: the lowest lane with the greatest key, and
+// its first position with it, is the lowest index.  Each of the k rounds takes
+// the maximum of the lanes' heads with one redux and refreshes the winner's head;
+// lane j ends with slot j.
+// Bound by instructions issued: T = 8192, E = 256, k = 8 in 8 groups reads 8.4 MB.
+template <int CPL, typename In>
+__global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
+  griddep_wait();
+  griddep_launch();
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const In* row = static_cast<const In*>(a.logits) + static_cast<long long>(t) * a.ld;
+  const int g = lane / a.lpg, sub = lane - g * a.lpg;
+  const int first = g * a.gs + sub * a.cpl;
+  const int count = g < a.n_groups ? max(0, min(a.cpl, a.gs - sub * a.cpl)) : 0;
+  const bool groups = a.topk_groups < a.n_groups;
+
+  float l[CPL];
+  constexpr int kPer16 = 16 / sizeof(In);
+  bool loaded = false;
+  if constexpr (CPL >= kPer16) if (a.vec) {
+    loaded = true;
+    // count is cpl or 0 here, and cpl a multiple of kPer16.
+#pragma unroll
+    for (int i = 0; i < CPL; i += kPer16) {
+      union { uint4 u; In e[kPer16]; } v;
+      v.u = make_uint4(0, 0, 0, 0);
+      if (i < count) v.u = *reinterpret_cast<const uint4*>(row + first + i);
+#pragma unroll
+      for (int z = 0; z < kPer16; ++z) l[i + z] = i + z < count ? to_float(v.e[z]) : -INFINITY;
+    }
+  }
+  if (!loaded) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) l[i] = i < count ? to_float(row[first + i]) : -INFINITY;
+  }
+
+  // Softmax over the whole row where a value of it is needed.
+  float rmax = 0.f, rsum = 1.f;
+  if (a.softmax && (!a.renorm || a.bias != nullptr || (groups && a.group_top == 2))) {
+    rmax = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) rmax = fmaxf(rmax, l[i]);   // fmaxf drops a NaN
+    rmax = warp_max(rmax);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      if (l[i] > -INFINITY) s += expf(l[i] - rmax);
+    rsum = warp_sum(s);
+  }
+  auto score = [&](float v) { return a.softmax ? expf(v - rmax) / rsum : sigmoid_f32(v); };
+
+  uint32_t key[CPL];
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i)
+      key[i] = (i < count && l[i] > -INFINITY) ? key_of(score(l[i]) + a.bias[first + i]) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) key[i] = key_of(l[i]);
+  }
+
+  bool close = false;   // an order that fp32 cannot decide
+  if (groups) {
+    uint32_t m1 = 0, m2 = 0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      m2 = max(m2, min(m1, key[i]));
+      m1 = max(m1, key[i]);
+    }
+    for (int o = 1; o < a.lpg; o <<= 1) {
+      const uint32_t o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
+      m2 = max(max(m2, o2), min(m1, o1));
+      m1 = max(m1, o1);
+    }
+    uint32_t gscore = m1;
+    if (a.group_top == 2 && m1 != 0) {
+      // Keys are logits without a bias; the sum is of their scores.
+      const float v1 = a.bias != nullptr ? value_of(m1) : score(value_of(m1));
+      const float v2 = m2 == 0 ? 0.f : (a.bias != nullptr ? value_of(m2) : score(value_of(m2)));
+      gscore = order_of(v1 + v2);
+    }
+    int rank = 0;
+    for (int q = 0; q < a.n_groups; ++q) {
+      const uint32_t sq = __shfl_sync(kFull, gscore, q * a.lpg);
+      rank += (sq > gscore || (sq == gscore && q < g)) ? 1 : 0;
+    }
+    const bool stays = rank < a.topk_groups;
+    if (a.bias != nullptr || a.group_top == 2) {
+      const uint32_t worst = __reduce_min_sync(kFull, g < a.n_groups && stays ? gscore : 0xffffffffu);
+      const uint32_t best = __reduce_max_sync(kFull, g < a.n_groups && !stays ? gscore : 0u);
+      if (best != 0 && worst != 0xffffffffu) {
+        const float vw = value_of(worst), vb = value_of(best);
+        close = vw - vb <= 2.f * close_bound(vw);
+      }
+    }
+    if (!stays) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) key[i] = 0;
+    }
+  }
+
+  int chosen = -1;
+  uint32_t head = 0;
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) head = max(head, key[i]);
+  // With fp32 keys one round more than k: the first expert left out.
+  const int rounds = a.bias != nullptr ? a.k + 1 : a.k;
+  uint32_t prev = 0;
+  for (int j = 0; j < rounds; ++j) {
+    const uint32_t m = __reduce_max_sync(kFull, head);
+    if (m == 0) break;
+    if (a.bias != nullptr && j > 0) close |= value_of(prev) - value_of(m) <= close_bound(value_of(prev));
+    prev = m;
+    if (j == a.k) break;
+    const int win = __ffs(__ballot_sync(kFull, head == m)) - 1;
+    int e = -1;
+    if (lane == win) {
+      head = 0;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) {
+        if (e < 0 && key[i] == m) { e = first + i; key[i] = 0; }
+        head = max(head, key[i]);
+      }
+    }
+    e = __shfl_sync(kFull, e, win);
+    if (lane == j) chosen = e;
+  }
+  if (close) chosen = select_exact<CPL, In>(a, row, lane, first, count);   // uniform over the warp
+
+  // Weights: lane j has slot j.
+  const bool have = chosen >= 0;
+  const float lj = have ? to_float(row[chosen]) : -INFINITY;
+  float w = 0.f;
+  if (a.renorm) {
+    float s = 0.f;
+    if (a.softmax) {
+      const float m = warp_max(lj);
+      s = have ? expf(lj - m) : 0.f;
+    } else {
+      s = have ? sigmoid_f32(lj) : 0.f;
+      // Far below zero a sigmoid is the exponential: shift it, so that nothing
+      // underflows (and the sum is never zero).
+      const float m = warp_max(lj);
+      if (m < -60.f) s = have ? expf(lj - m) : 0.f;
+    }
+    const float total = warp_sum(s);
+    w = have ? s / total * a.scale : 0.f;
+  } else if (have) {
+    w = score(lj) * a.scale;
+  }
+  if (lane < a.k) {
+    a.idx[static_cast<long long>(t) * a.k + lane] = chosen;
+    a.w[static_cast<long long>(t) * a.k + lane] = w;
+  }
+}
+
+// Gradient of the weights with respect to the logits, one warp per token.  With
+// u_j = dw_j (slots of one expert added in slot order):
+//   softmax, renormalised   dl_j = w_j (dw_j - sum_i dw_i w_i / scale), chosen only
+//   softmax                 dl_e = scale p_e (u_e - sum_j dw_j p_j), every expert
+//   sigmoid                 dl_j = ds_j s_j (1 - s_j), ds_j = scale dw_j, or
+//                           scale (dw_j - sum_i dw_i s_i / S) / S with S = sum s_i
+// The row is written once (zeros, or the softmax's common term); the chosen
+// experts' lanes then write theirs.
+// Bound by memory: every logit of the row is written, and read for a plain
+// softmax (T = 16384, E = 128 fp32: 17.8 MB).
+template <int PER, int VEC, typename In>
+__global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
+  griddep_wait();
+  griddep_launch();
+  const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (t >= a.T) return;
+  const In* row = static_cast<const In*>(a.logits) + static_cast<long long>(t) * a.ld;
+  In* out = static_cast<In*>(a.dlogits) + static_cast<long long>(t) * a.ld_out;
+  struct alignas(sizeof(In) * VEC) Vec { In e[VEC]; };
+  const bool whole = a.softmax && !a.renorm;
+
+  int e = -1;
+  float dw = 0.f;
+  if (lane < a.k) {
+    e = a.idx[static_cast<long long>(t) * a.k + lane];
+    dw = a.dw[static_cast<long long>(t) * a.k + lane];
+    if (e < 0 || e >= a.E) { e = -1; dw = 0.f; }
+  }
+  const float lj = e >= 0 ? to_float(row[e]) : -INFINITY;
+  // -inf and NaN logits are never chosen; an index given for one gets no gradient.
+  const bool have = lj > -INFINITY;
+
+  auto store = [](float v) {
+    if constexpr (sizeof(In) == 2) return static_cast<In>(pack_bf16x2(v, 0.f) & 0xFFFFu);
+    else return v;
+  };
+
+  float l[PER];
+  float rmax = -INFINITY, rsum = 1.f;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < PER; i += VEC) {
+      const int c = (i * 32 + lane * VEC);
+      Vec v;
+#pragma unroll
+      for (int z = 0; z < VEC; ++z) l[i + z] = -INFINITY;
+      if (c < a.E) {
+        v = *reinterpret_cast<const Vec*>(row + c);
+#pragma unroll
+        for (int z = 0; z < VEC; ++z) l[i + z] = to_float(v.e[z]);
+      }
+#pragma unroll
+      for (int z = 0; z < VEC; ++z) rmax = fmaxf(rmax, l[i + z]);
+    }
+    rmax = warp_max(rmax);
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      l[i] = l[i] > -INFINITY ? expf(l[i] - rmax) : 0.f;
+      s += l[i];
+    }
+    rsum = warp_sum(s);
+  }
+
+  float dl = 0.f, common = 0.f;   // common: -sum_j dw_j p_j
+  float p = 0.f;
+  if (whole) {
+    p = have ? expf(lj - rmax) / rsum : 0.f;
+    common = -warp_sum(dw * p);
+    dl = p * dw;
+  } else if (a.softmax) {
+    const float m = warp_max(lj);
+    const float s = have ? expf(lj - m) : 0.f;
+    const float total = warp_sum(s);
+    const float q = have ? s / total : 0.f;
+    const float mean = warp_sum(dw * q);
+    dl = q * (dw - mean);
+  } else {
+    float s = have ? sigmoid_f32(lj) : 0.f;
+    // 1 - s without cancellation: sigmoid(-l).
+    const float c = have ? sigmoid_f32(-lj) : 0.f;
+    if (a.renorm) {
+      const float m = warp_max(lj);
+      if (m < -60.f) s = have ? expf(lj - m) : 0.f;   // as the forward pass does
+      const float total = warp_sum(s);
+      const float q = have ? s / total : 0.f;
+      const float mean = warp_sum(dw * q);
+      dl = q * c * (dw - mean);
+    } else {
+      dl = s * c * dw;
+    }
+  }
+  // Slots that name the same expert add up, in slot order.
+  float mine = 0.f;
+  for (int j = 0; j < a.k; ++j) {
+    const int ej = __shfl_sync(kFull, e, j);
+    const float dj = __shfl_sync(kFull, dl, j);
+    if (ej == e) mine += dj;
+  }
+  if (whole && have) mine += p * common;
+  mine *= a.scale;
+  const float base = whole ? common * a.scale / rsum : 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; i += VEC) {
+    const int c = (i * 32 + lane * VEC);
+    if (c >= a.E) break;
+    Vec v;
+#pragma unroll
+    for (int z = 0; z < VEC; ++z) v.e[z] = store(whole && l[i + z] > 0.f ? l[i + z] * base : 0.f);
+    *reinterpret_cast<Vec*>(out + c) = v;
+  }
+  __syncwarp();
+  if (have) out[e] = store(mine);
+}
+
+// ---------------------------------------------------------------- grouping
+// One cluster of 8 CTAs; CTA c takes the c-th eighth of the flattened (token,
+// slot) list and each of its warps a run of it.  A warp walks its run 32 entries
+// at a time (match.any ranks equal experts inside them) counting per expert in
+// its own row of shared memory; the prefix over warps, over CTAs (through
+// distributed shared memory) and over experts gives every warp its first row of
+// every expert; a second walk hands the rows out.  Integers only, the order is the
+// list's: stable by token, then slot.  No workspace and one launch, whatever T.
+// Bound by latency: the list is small (T = 8192, k = 8: 262 KB).
+constexpr int kGroupCtas = 8;
+constexpr int kGroupThreads = 1024;
+
+__global__ void __launch_bounds__(kGroupThreads)
+    k_group_rows(const int32_t* idx, int n, int k, int E, int32_t* offsets,
+                 int32_t* token_of_row, int32_t* row_of_slot) {
+  extern __shared__ int32_t gsm[];
+  constexpr int kWarps = kGroupThreads / 32;
+  int32_t* hist = gsm;                  // [kWarps][E]
+  int32_t* mine = gsm + kWarps * E;     // [E] this CTA's counts (read by the others)
+  __shared__ int32_t warp_tot[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cta = static_cast<int>(cluster_ctarank());
+  // Runs are whole multiples of 32 entries.
+  const long long per_warp = ((static_cast<long long>(n) + kGroupCtas * kWarps - 1) / (kGroupCtas * kWarps) + 31) / 32 * 32;
+  const long long lo = min(static_cast<long long>(n), (static_cast<long long>(cta) * kWarps + warp) * per_warp);
+  const long long hi = min(static_cast<long long>(n), lo + per_warp);
+  for (int i = tid; i < kWarps * E; i += kGroupThreads) hist[i] = 0;
+  griddep_wait();
+  griddep_launch();
+  __syncthreads();
+
+  int32_t* h = hist + warp * E;
+  for (long long b = lo; b < hi; b += 32) {
+    const long long i = b + lane;
+    const int e = i < hi ? idx[i] : -1;
+    const bool ok = e >= 0 && e < E;
+    const unsigned same = __match_any_sync(kFull, ok ? e : -1);
+    if (ok && lane == __ffs(same) - 1) h[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kGroupThreads) {
+    int run = 0;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) {
+      const int c = hist[w * E + e];
+      hist[w * E + e] = run;
+      run += c;
+    }
+    mine[e] = run;
+  }
+  cluster_sync();
+  // kGroupThreads >= E: thread e has expert e.
+  int before = 0, total = 0;
+  if (tid < E) {
+#pragma unroll
+    for (int c = 0; c < kGroupCtas; ++c) {
+      int v;
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(mine + tid, c)));
+      if (c < cta) before += v;
+      total += v;
+    }
+  }
+  int incl = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_tot[warp] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+#pragma unroll 8
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) base += warp_tot[w];
+    all += warp_tot[w];
+  }
+  const int start = base + incl - total;
+  if (tid < E) {
+    if (cta == 0) {
+      offsets[tid] = start;
+      if (tid == E - 1) offsets[E] = all;
+    }
+    const int add = start + before;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) hist[w * E + tid] += add;
+  }
+  __syncthreads();
+  for (long long b = lo; b < hi; b += 32) {
+    const long long i = b + lane;
+    const int e = i < hi ? idx[i] : -1;
+    const bool ok = e >= 0 && e < E;
+    const unsigned same = __match_any_sync(kFull, ok ? e : -1);
+    int pos = -1;
+    if (ok) pos = h[e] + __popc(same & ((1u << lane) - 1u));
+    __syncwarp();
+    if (ok && lane == __ffs(same) - 1) h[e] += __popc(same);
+    __syncwarp();
+    if (i < hi) {
+      row_of_slot[i] = pos;
+      if (ok) token_of_row[pos] = static_cast<int32_t>(i / k);
+    }
+  }
+  // Rows behind the last group come from no token.
+  for (long long r = all + static_cast<long long>(cta) * kGroupThreads + tid; r < n; r += kGroupCtas * kGroupThreads)
+    token_of_row[r] = -1;
+  cluster_sync();   // no CTA leaves while another may still read its counts
+}
+
+template <typename In>
+cudaError_t route_by_width(const RouteOpArgs& a, cudaStream_t s) {
+  const dim3 grid((a.T + 7) / 8), block(256);
+  if (a.cpl <= 2) return launch_k(k_route<2, In>, grid, block, 0, s, false, a);
+  if (a.cpl <= 4) return launch_k(k_route<4, In>, grid, block, 0, s, false, a);
+  if (a.cpl <= 8) return launch_k(k_route<8, In>, grid, block, 0, s, false, a);
+  if (a.cpl <= 16) return launch_k(k_route<16, In>, grid, block, 0, s, false, a);
+  return launch_k(k_route<32, In>, grid, block, 0, s, false, a);
+}
+
+template <int VEC, typename In>
+cudaError_t route_back_by_width(const RouteBackArgs& a, cudaStream_t s) {
+  const dim3 grid((a.T + 7) / 8), block(256);
+  if (a.E <= 128) return launch_k(k_route_backward<4, VEC, In>, grid, block, 0, s, false, a);
+  if (a.E <= 256) return launch_k(k_route_backward<8, VEC, In>, grid, block, 0, s, false, a);
+  if (a.E <= 512) return launch_k(k_route_backward<16, VEC, In>, grid, block, 0, s, false, a);
+  return launch_k(k_route_backward<32, VEC, In>, grid, block, 0, s, false, a);
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteOpArgs& a, bool bf16, cudaStream_t s) {
+  return bf16 ? route_by_width<uint16_t>(a, s) : route_by_width<float>(a, s);
+}
+
+cudaError_t launch_route_backward(const RouteBackArgs& a, bool bf16, cudaStream_t s) {
+  if (a.vec) return bf16 ? route_back_by_width<4, uint16_t>(a, s) : route_back_by_width<4, float>(a, s);
+  return bf16 ? route_back_by_width<1, uint16_t>(a, s) : route_back_by_width<1, float>(a, s);
+}
+
+cudaError_t launch_group_rows(const int32_t* idx, int T, int k, int E, int32_t* offsets, int32_t* token_of_row,
+                              int32_t* row_of_slot, cudaStream_t s) {
+  const size_t smem = static_cast<size_t>(kGroupThreads / 32 + 1) * E * sizeof(int32_t);
+  const cudaError_t rc = cudaFuncSetAttribute(k_group_rows, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (kGroupThreads / 32 + 1) * kRouteMaxE * 4);
+  if (rc != cudaSuccess) return rc;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kGroupCtas);
+  cfg.blockDim = dim3(kGroupThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kGroupCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_group_rows, idx, T * k, k, E, offsets, token_of_row, row_of_slot);
+}
+
+}  // namespace moe

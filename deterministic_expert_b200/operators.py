@@ -1,0 +1,388 @@
+"""Handle-free expert-layer operators: routing and its gradient, grouping, E4M3
+quantisation with one scale per 128 elements, block-scaled E4M3 products, and the
+weighted combine with its gradient (include/moe.h documents the entry points).
+
+Like the rest of the binding these functions only check and marshal arguments.
+Outputs are allocated where they are not given; ``stream`` (default: the current
+stream of the tensors' device) is where the kernels run, and where outputs are
+allocated.  Tensors of a call live on one CUDA device, which need not be the
+current one.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+import deterministic_expert_b200 as _moe
+
+DTYPE_BF16, DTYPE_F32 = 0, 1
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32}
+BLOCK = 128          # elements that share a scale
+
+
+class moe_route_config(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("scores", ctypes.c_int), ("n_groups", ctypes.c_int),
+                ("topk_groups", ctypes.c_int), ("group_top", ctypes.c_int), ("renormalize", ctypes.c_int),
+                ("routed_scale", ctypes.c_float), ("logits_dtype", ctypes.c_int)]
+
+
+class moe_glu_config(ctypes.Structure):
+    _fields_ = [("activation", ctypes.c_int), ("gate_clamp_max", ctypes.c_float), ("up_clamp", ctypes.c_float),
+                ("situ_beta_gate", ctypes.c_float), ("situ_beta_up", ctypes.c_float)]
+
+
+_vp, _i, _ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
+ARGTYPES = {
+    "moe_route": [ctypes.POINTER(moe_route_config), _i, _vp, _ll, _vp, _vp, _vp, _vp],
+    "moe_route_backward": [ctypes.POINTER(moe_route_config), _i, _vp, _ll, _vp, _vp, _vp, _ll, _vp],
+    "moe_group_rows": [_i, _i, _i, _vp, _vp, _vp, _vp, _vp],
+    "moe_quantize_rows_fp8": [_i, _i, _vp, _i, _ll, _i, _vp, _vp, _vp, _vp, _ll, _vp],
+    "moe_quantize_weights_fp8": [_i, _i, _i, _vp, _vp, _vp, _vp],
+    "moe_glu_quantize_fp8": [ctypes.POINTER(moe_glu_config), _i, _i, _vp, _ll, _vp, _vp, _vp, _ll, _vp],
+    "moe_glu_backward_quantize_fp8": [ctypes.POINTER(moe_glu_config), _i, _i, _vp, _ll, _vp, _ll, _vp, _vp, _vp,
+                                      _ll, _vp],
+    "moe_matmul_fp8": [_i, _i, _vp, _i, _i, _i, _vp, _vp, _ll, _vp, _vp, _vp, _i, _ll, _vp],
+    "moe_combine_rows": [_i, _i, _i, _i, _vp, _i, _ll, _vp, _vp, _vp, _vp, _i, _vp],
+    "moe_combine_rows_backward": [_i, _i, _i, _i, _vp, _vp, _i, _ll, _vp, _vp, _vp, _vp, _vp],
+    "moe_get_operator_error": [_vp],
+}
+_fns: dict = {}
+
+
+def _fn(name):
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(_moe.lib(), name)
+        f.argtypes = ARGTYPES[name]
+        _fns[name] = f
+    return f
+
+
+def _call(name, device, stream, *args):
+    """Run an entry point with the tensors' device current, on `stream`."""
+    f = _fn(name)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            rc = f(*args, _on(stream, device))
+    else:
+        rc = f(*args, _on(stream, device))
+    if rc != 0:
+        raise _moe.MoEError(rc, name)
+
+
+def _on(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _alloc(stream, device):
+    """Outputs belong to the stream that writes them."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(_moe._torch_stream(stream, device))
+
+
+def _need(cond, what):
+    if not cond:
+        raise ValueError(what)
+
+
+def _tensor(t, name, device, dtypes, shape=None, contiguous=True):
+    """Refuse a tensor the library would read or write wrongly."""
+    _need(isinstance(t, torch.Tensor), f"{name}: expected a tensor")
+    _need(t.is_cuda and (device is None or t.device == device),
+          f"{name}: expected a CUDA tensor" + (f" on {device}, got {t.device}" if device is not None else ""))
+    _need(t.dtype in dtypes, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape is not None:
+        _need(tuple(t.shape) == tuple(shape), f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous:
+        _need(t.is_contiguous(), f"{name}: expected a contiguous tensor")
+
+
+def _rows(t, name):
+    """Row pitch of a matrix whose rows are dense."""
+    _need(t.dim() == 2, f"{name}: expected two dimensions, got {t.dim()}")
+    _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: expected rows of neighbouring elements")
+    if t.shape[0] <= 1:
+        return max(int(t.shape[1]), 1)
+    _need(t.stride(0) >= t.shape[1], f"{name}: rows overlap")
+    return int(t.stride(0))
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
+
+
+def _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale):
+    _need(scores in ("softmax", "sigmoid"), f"scores: expected 'softmax' or 'sigmoid', got {scores!r}")
+    return moe_route_config(E, int(k), _moe.ROUTER_SOFTMAX if scores == "softmax" else _moe.ROUTER_SIGMOID_BIAS,
+                            int(n_groups), int(topk_groups), int(group_top), 1 if renormalize else 0,
+                            float(routed_scale), _DTYPES[logits.dtype])
+
+
+def route(logits, k: int, *, scores: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
+          group_top: int = 2, renormalize: bool = False, routed_scale: float = 1.0, out_idx=None, out_w=None,
+          stream=None):
+    """moe_route: the k experts of every row of ``logits`` [T, E] (bf16 or fp32) and
+    their weights: (idx int32 [T, k], w fp32 [T, k])."""
+    _tensor(logits, "logits", None, tuple(_DTYPES), contiguous=False)
+    ld = _rows(logits, "logits")
+    dev = logits.device
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    if bias is not None:
+        _tensor(bias, "bias", dev, _F32, (E,))
+    cfg = _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
+    _need(cfg.k >= 0, "k: negative")
+    if out_idx is None or out_w is None:
+        with _alloc(stream, dev):
+            out_idx = torch.empty((T, cfg.k), dtype=torch.int32, device=dev) if out_idx is None else out_idx
+            out_w = torch.empty((T, cfg.k), dtype=torch.float32, device=dev) if out_w is None else out_w
+    _tensor(out_idx, "out_idx", dev, _I32, (T, cfg.k))
+    _tensor(out_w, "out_w", dev, _F32, (T, cfg.k))
+    _call("moe_route", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld,
+          None if bias is None else bias.data_ptr(), out_idx.data_ptr(), out_w.data_ptr())
+    return out_idx, out_w
+
+
+def route_backward(logits, idx, dw, *, scores: str = "softmax", n_groups: int = 1, topk_groups: int = 1,
+                   group_top: int = 2, renormalize: bool = False, routed_scale: float = 1.0, out=None, stream=None):
+    """moe_route_backward: the gradient of ``logits`` from ``dw``, that of the weights
+    ``route`` gave for the experts ``idx`` with the same arguments."""
+    _tensor(logits, "logits", None, tuple(_DTYPES), contiguous=False)
+    ld = _rows(logits, "logits")
+    dev = logits.device
+    T, E = int(logits.shape[0]), int(logits.shape[1])
+    _need(idx.dim() == 2, "idx: expected two dimensions")
+    k = int(idx.shape[1])
+    _tensor(idx, "idx", dev, _I32, (T, k))
+    _tensor(dw, "dw", dev, _F32, (T, k))
+    cfg = _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
+    if out is None:
+        with _alloc(stream, dev):
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    _tensor(out, "out", dev, (logits.dtype,), (T, E), contiguous=False)
+    _call("moe_route_backward", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld, idx.data_ptr(),
+          dw.data_ptr(), out.data_ptr(), _rows(out, "out"))
+    return out
+
+
+def group_rows(idx, E: int, *, out=None, stream=None):
+    """moe_group_rows: ``idx`` [T, k] int32 -> (offsets [E + 1], token_of_row [T k],
+    row_of_slot [T, k]), all int32.  ``out``: the three tensors to write."""
+    _tensor(idx, "idx", None, _I32)
+    _need(idx.dim() == 2, "idx: expected two dimensions")
+    dev = idx.device
+    T, k = int(idx.shape[0]), int(idx.shape[1])
+    if out is None:
+        with _alloc(stream, dev):
+            out = (torch.empty(max(int(E), 0) + 1, dtype=torch.int32, device=dev),
+                   torch.empty(T * k, dtype=torch.int32, device=dev),
+                   torch.empty((T, k), dtype=torch.int32, device=dev))
+    offsets, token_of_row, row_of_slot = out
+    _tensor(offsets, "offsets", dev, _I32, (int(E) + 1,))
+    _tensor(token_of_row, "token_of_row", dev, _I32, (T * k,))
+    _tensor(row_of_slot, "row_of_slot", dev, _I32, (T, k))
+    _call("moe_group_rows", dev, stream, T, k, int(E), idx.data_ptr(), offsets.data_ptr(), token_of_row.data_ptr(),
+          row_of_slot.data_ptr())
+    return offsets, token_of_row, row_of_slot
+
+
+def _quant_out(R, K, out_codes, out_scales, dev, stream):
+    nb = -(-K // BLOCK)
+    if out_codes is None or out_scales is None:
+        with _alloc(stream, dev):
+            out_codes = torch.empty((R, K), dtype=torch.uint8, device=dev) if out_codes is None else out_codes
+            out_scales = torch.empty((nb, R), dtype=torch.float32, device=dev) if out_scales is None else out_scales
+    _tensor(out_codes, "out_codes", dev, _CODES, (R, K))
+    _tensor(out_scales, "out_scales", dev, _F32, (nb, R), contiguous=False)
+    return out_codes, out_scales, _rows(out_scales, "out_scales")
+
+
+def _count(n_rows, dev):
+    if n_rows is None:
+        return None
+    _tensor(n_rows, "n_rows", dev, _I32)
+    _need(n_rows.numel() == 1, "n_rows: expected one element")
+    return n_rows.data_ptr()
+
+
+def quantize_rows_fp8(x, *, token_of_row=None, n_rows=None, out_codes=None, out_scales=None, stream=None):
+    """moe_quantize_rows_fp8: rows of ``x`` [M, K] (bf16 or fp32; row r from row
+    token_of_row[r] if given) -> (E4M3 codes uint8 [R, K], scales fp32
+    [ceil(K / 128), R])."""
+    _tensor(x, "x", None, tuple(_DTYPES), contiguous=False)
+    ld = _rows(x, "x")
+    dev = x.device
+    M, K = int(x.shape[0]), int(x.shape[1])
+    R = M
+    if token_of_row is not None:
+        _need(token_of_row.dim() == 1, "token_of_row: expected one dimension")
+        _tensor(token_of_row, "token_of_row", dev, _I32)
+        R = int(token_of_row.shape[0])
+    out_codes, out_scales, ld_s = _quant_out(R, K, out_codes, out_scales, dev, stream)
+    _call("moe_quantize_rows_fp8", dev, stream, R, K, x.data_ptr(), _DTYPES[x.dtype], ld, M,
+          None if token_of_row is None else token_of_row.data_ptr(), _count(n_rows, dev), out_codes.data_ptr(),
+          out_scales.data_ptr(), max(ld_s, R))
+    return out_codes, out_scales
+
+
+def quantize_weights_fp8(w, *, out_codes=None, out_scales=None, stream=None):
+    """moe_quantize_weights_fp8: bf16 weights [G, N, K] (or [N, K]) -> (E4M3 codes
+    uint8 of the same shape, scales fp32 [G, ceil(N / 128), ceil(K / 128)])."""
+    _tensor(w, "w", None, _BF16)
+    _need(w.dim() in (2, 3), "w: expected two or three dimensions")
+    dev = w.device
+    N, K = int(w.shape[-2]), int(w.shape[-1])
+    G = int(w.shape[0]) if w.dim() == 3 else 1
+    sshape = tuple(w.shape[:-2]) + (-(-N // BLOCK), -(-K // BLOCK))
+    if out_codes is None or out_scales is None:
+        with _alloc(stream, dev):
+            out_codes = torch.empty(w.shape, dtype=torch.uint8, device=dev) if out_codes is None else out_codes
+            out_scales = torch.empty(sshape, dtype=torch.float32, device=dev) if out_scales is None else out_scales
+    _tensor(out_codes, "out_codes", dev, _CODES, w.shape)
+    _tensor(out_scales, "out_scales", dev, _F32, sshape)
+    _call("moe_quantize_weights_fp8", dev, stream, G, N, K, w.data_ptr(), out_codes.data_ptr(), out_scales.data_ptr())
+    return out_codes, out_scales
+
+
+def _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up):
+    return moe_glu_config(int(activation), float(gate_clamp_max), float(up_clamp), float(situ_beta_gate),
+                          float(situ_beta_up))
+
+
+def _gate_up(gu):
+    _tensor(gu, "gu", None, _BF16, contiguous=False)
+    ld = _rows(gu, "gu")
+    _need(gu.shape[1] % 2 == 0, "gu: expected [gate | up] columns")
+    return ld, int(gu.shape[0]), int(gu.shape[1]) // 2
+
+
+def glu_quantize_fp8(gu, *, activation: int = 0, gate_clamp_max: float = float("inf"), up_clamp: float = float("inf"),
+                     situ_beta_gate: float = 4.0, situ_beta_up: float = 25.0, n_rows=None, out_codes=None,
+                     out_scales=None, stream=None):
+    """moe_glu_quantize_fp8: rows [gate | up] (bf16 [R, 2 I]) -> the gated unit as
+    (E4M3 codes [R, I], scales [ceil(I / 128), R])."""
+    ld, R, I = _gate_up(gu)
+    dev = gu.device
+    cfg = _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up)
+    out_codes, out_scales, ld_s = _quant_out(R, I, out_codes, out_scales, dev, stream)
+    _call("moe_glu_quantize_fp8", dev, stream, ctypes.byref(cfg), R, I, gu.data_ptr(), ld, _count(n_rows, dev),
+          out_codes.data_ptr(), out_scales.data_ptr(), max(ld_s, R))
+    return out_codes, out_scales
+
+
+def glu_backward_quantize_fp8(gu, dh, *, activation: int = 0, gate_clamp_max: float = float("inf"),
+                              up_clamp: float = float("inf"), situ_beta_gate: float = 4.0, situ_beta_up: float = 25.0,
+                              n_rows=None, out_codes=None, out_scales=None, stream=None):
+    """moe_glu_backward_quantize_fp8: the gradient of ``gu`` from ``dh`` (bf16 [R, I]),
+    that of the gated unit, as (E4M3 codes [R, 2 I], scales [2 I / 128, R])."""
+    ld, R, I = _gate_up(gu)
+    dev = gu.device
+    _tensor(dh, "dh", dev, _BF16, (R, I), contiguous=False)
+    cfg = _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up)
+    out_codes, out_scales, ld_s = _quant_out(R, 2 * I, out_codes, out_scales, dev, stream)
+    _call("moe_glu_backward_quantize_fp8", dev, stream, ctypes.byref(cfg), R, I, gu.data_ptr(), ld, dh.data_ptr(),
+          _rows(dh, "dh"), _count(n_rows, dev), out_codes.data_ptr(), out_scales.data_ptr(), max(ld_s, R))
+    return out_codes, out_scales
+
+
+def matmul_fp8(a, a_scale, w, w_scale, *, offsets=None, transposed: bool = False, out=None,
+               out_dtype=torch.bfloat16, stream=None):
+    """moe_matmul_fp8: E4M3 rows ``a`` [M, K] with ``a_scale`` [ceil(K / 128), M] times
+    E4M3 weights ``w`` [G, N, K] (or [N, K]) with ``w_scale`` [G, ceil(N / 128),
+    ceil(K / 128)] -> [M, N]; transposed: ``a`` [M, N] -> [M, K].  ``offsets`` int32
+    [G + 1]: the rows that meet each group."""
+    _tensor(a, "a", None, _CODES)
+    _need(a.dim() == 2, "a: expected two dimensions")
+    dev = a.device
+    _tensor(w, "w", dev, _CODES)
+    _need(w.dim() in (2, 3), "w: expected two or three dimensions")
+    M, con = int(a.shape[0]), int(a.shape[1])
+    N, K = int(w.shape[-2]), int(w.shape[-1])
+    G = int(w.shape[0]) if w.dim() == 3 else 1
+    width = K if transposed else N
+    _need(con == (N if transposed else K), f"a: expected {N if transposed else K} columns, got {con}")
+    _tensor(a_scale, "a_scale", dev, _F32, (-(-con // BLOCK), M), contiguous=False)
+    ld_as = _rows(a_scale, "a_scale")
+    _tensor(w_scale, "w_scale", dev, _F32, tuple(w.shape[:-2]) + (-(-N // BLOCK), -(-K // BLOCK)))
+    if offsets is not None:
+        _tensor(offsets, "offsets", dev, _I32, (G + 1,))
+    else:
+        _need(G == 1, "offsets: needed with more than one group")
+    if out is None:
+        _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
+        with _alloc(stream, dev):
+            out = torch.empty((M, width), dtype=out_dtype, device=dev)
+    _tensor(out, "out", dev, tuple(_DTYPES), (M, width), contiguous=False)
+    _call("moe_matmul_fp8", dev, stream, 1 if transposed else 0, G, None if offsets is None else offsets.data_ptr(),
+          M, N, K, a.data_ptr(), a_scale.data_ptr(), max(ld_as, M), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
+          _DTYPES[out.dtype], max(_rows(out, "out"), width))
+    return out
+
+
+def _slots(row_of_slot, w, dev):
+    _need(row_of_slot.dim() == 2, "row_of_slot: expected two dimensions")
+    T, k = int(row_of_slot.shape[0]), int(row_of_slot.shape[1])
+    _tensor(row_of_slot, "row_of_slot", dev, _I32, (T, k))
+    if w is not None:
+        _tensor(w, "w", dev, _F32, (T, k))
+    return T, k
+
+
+def combine_rows(y, row_of_slot, w=None, *, addend=None, out=None, out_dtype=torch.bfloat16, stream=None):
+    """moe_combine_rows: out[t] = addend[t] + sum_j w[t, j] y[row_of_slot[t, j]]
+    (``w`` None: every slot 1), fp32 sums, [T, D] of ``out_dtype``."""
+    _tensor(y, "y", None, tuple(_DTYPES), contiguous=False)
+    ld = _rows(y, "y")
+    dev = y.device
+    rows, D = int(y.shape[0]), int(y.shape[1])
+    T, k = _slots(row_of_slot, w, dev)
+    if addend is not None:
+        _tensor(addend, "addend", dev, _BF16, (T, D))
+    if out is None:
+        _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
+        with _alloc(stream, dev):
+            out = torch.empty((T, D), dtype=out_dtype, device=dev)
+    _tensor(out, "out", dev, tuple(_DTYPES), (T, D))
+    _call("moe_combine_rows", dev, stream, T, k, D, rows, y.data_ptr(), _DTYPES[y.dtype], max(ld, D),
+          row_of_slot.data_ptr(), None if w is None else w.data_ptr(),
+          None if addend is None else addend.data_ptr(), out.data_ptr(), _DTYPES[out.dtype])
+    return out
+
+
+def combine_rows_backward(dout, y, row_of_slot, w=None, *, need_dw: bool = True, out_dy=None, out_dw=None,
+                          stream=None):
+    """moe_combine_rows_backward: (dy, dw) from ``dout`` (bf16 [T, D]), the gradient of
+    ``combine_rows(y, row_of_slot, w)``; dy has the type of ``y``, dw is fp32 [T, k]
+    (None with need_dw False)."""
+    _tensor(y, "y", None, tuple(_DTYPES), contiguous=False)
+    ld = _rows(y, "y")
+    dev = y.device
+    rows, D = int(y.shape[0]), int(y.shape[1])
+    T, k = _slots(row_of_slot, w, dev)
+    _tensor(dout, "dout", dev, _BF16, (T, D))
+    with _alloc(stream, dev):
+        if out_dy is None:
+            # The pitch of y, as the entry point has one for both.
+            out_dy = torch.empty((rows, ld), dtype=y.dtype, device=dev)[:, :D]
+        if need_dw and out_dw is None:
+            out_dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _tensor(out_dy, "out_dy", dev, (y.dtype,), (rows, D), contiguous=False)
+    _need(rows <= 1 or _rows(out_dy, "out_dy") == ld, "out_dy: expected the row pitch of y")
+    if need_dw:
+        _tensor(out_dw, "out_dw", dev, _F32, (T, k))
+    _call("moe_combine_rows_backward", dev, stream, T, k, D, rows, dout.data_ptr(), y.data_ptr(), _DTYPES[y.dtype],
+          max(ld, D), row_of_slot.data_ptr(), None if w is None else w.data_ptr(), out_dy.data_ptr(),
+          out_dw.data_ptr() if need_dw else None)
+    return out_dy, (out_dw if need_dw else None)
+
+
+def operator_error(device=None, stream=None) -> int:
+    """moe_get_operator_error on ``device`` (default: the current one): read and clear
+    the error word of matmul_fp8.  Synchronises the stream."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with torch.cuda.device(dev):
+        return int(_fn("moe_get_operator_error")(_on(stream, dev)))

@@ -521,6 +521,160 @@ int moe_peer_close(void* dptr);
 int moe_peer_barrier(int world, int rank, uint32_t* const* flags, uint32_t epoch, int* err, int limit_us,
                      void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert-layer operators without a handle: the routing, grouping, quantisation,
+ * products and combine of a layer that a caller composes itself, with the
+ * gradients with respect to its inputs (the experts' E4M3 weights are as stored
+ * and have none).  A forward pass, T tokens of width D, E experts of width I:
+ *   moe_route            logits [T, E]                  -> idx, w [T, k]
+ *   moe_group_rows       idx                            -> offsets, token_of_row, row_of_slot
+ *   moe_quantize_rows_fp8 x, token_of_row               -> grouped E4M3 rows [T k, D]
+ *   moe_matmul_fp8       with [E, 2 I, D] (gate | up)   -> [T k, 2 I] bf16
+ *   moe_glu_quantize_fp8                                -> E4M3 rows [T k, I]
+ *   moe_matmul_fp8       with [E, D, I]                 -> [T k, D]
+ *   moe_combine_rows     w, row_of_slot                 -> [T, D]
+ * and backwards: moe_combine_rows_backward, moe_quantize_rows_fp8,
+ * moe_matmul_fp8 (transposed), moe_glu_backward_quantize_fp8, moe_matmul_fp8
+ * (transposed), moe_combine_rows (without weights), moe_route_backward.
+ *
+ * Every result row depends on its own inputs only, bit for bit: not on the
+ * number of rows, their grouping or the other rows.  No call allocates device
+ * memory, keeps a workspace or synchronises (moe_get_operator_error does); each
+ * may be captured into a graph.  Everything is read when the call's kernels run
+ * on `stream`, which belongs to the current device, as all pointers do.
+ * Matrices are row-major; rows are densely packed unless a row pitch ("ld", in
+ * elements) is given.  Unless noted a pointer to 8- or 16-byte vectors must be
+ * 16-byte aligned.  Rows = 0 (or T = 0) returns MOE_OK and launches nothing.
+ * Errors: MOE_EINVAL (NULL, misaligned, negative size, bad enum),
+ * MOE_EUNSUPPORTED (a size outside the limits given), MOE_ECUDA (launch).
+ * ------------------------------------------------------------------------ */
+typedef enum moe_dtype { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype;
+
+typedef struct moe_route_config {
+  int E;               /* experts, 1 .. 1024                                          */
+  int k;               /* experts per token, 1 .. min(E, 32)                          */
+  int scores;          /* MOE_ROUTER_SOFTMAX or MOE_ROUTER_SIGMOID_BIAS               */
+  int n_groups;        /* groups of E / n_groups neighbouring experts, 1 .. 32        */
+  int topk_groups;     /* groups that experts are chosen from, 1 .. n_groups          */
+  int group_top;       /* a group's score: the sum of its 1 or 2 largest keys         */
+  int renormalize;     /* 1: divide the chosen scores by their sum                    */
+  float routed_scale;  /* multiplies every weight                                     */
+  int logits_dtype;    /* moe_dtype                                                   */
+} moe_route_config;
+
+/* Routing: s = softmax(l) or sigmoid(l) over a row of logits, key = s + bias
+ * (bias [E] fp32 or NULL; it selects only).  With topk_groups < n_groups the
+ * best topk_groups groups stay; of their experts the k with the largest keys are
+ * chosen, in descending order; equal keys or group scores go to the lower index,
+ * and the order is that of exact arithmetic, not of rounded keys.  Weights are
+ * scores (over their sum if renormalize) times routed_scale, fp32.
+ * An expert whose logit or key is -inf or NaN is never chosen (nor counted in
+ * the softmax); slots without an expert get index -1 and weight 0, so a padding
+ * row is a row of -inf.  logits [T, ld], any alignment of their type.
+ * Limits: E divisible by n_groups; the experts of a group over the lanes of a
+ * warp that it gets (the power of two at most 32 / n_groups) at most 32 each.
+ * A moe_layer_forward router is the case n_groups = 1 (its softmax bias is one
+ * of the logits: add it before). */
+int moe_route(const moe_route_config* cfg, int T, const void* logits, long long ld, const float* bias,
+              int32_t* out_idx, float* out_w, void* stream);
+
+/* Its gradient: dlogits [T, ld_out] (type of the logits) from dw [T, k], the
+ * gradient of the weights, and the idx [T, k] that moe_route chose (entries
+ * outside [0, E) are skipped, an expert named twice gets both).  The choice and
+ * the bias have no gradient.  group fields of cfg are not used. */
+int moe_route_backward(const moe_route_config* cfg, int T, const void* logits, long long ld, const int32_t* idx,
+                       const float* dw, void* dlogits, long long ld_out, void* stream);
+
+/* Grouping: the (token, slot) rows of idx [T, k] in the order of their experts,
+ * inside an expert by token, then slot.  offsets [E + 1]: expert e has rows
+ * offsets[e] .. offsets[e + 1] - 1; token_of_row [T k]: a row's token, -1 behind
+ * the last row; row_of_slot [T, k]: a slot's row, -1 for an index outside [0, E).
+ * 1 <= E <= 1024, 1 <= k, T k < 2^31. */
+int moe_group_rows(int T, int k, int E, const int32_t* idx, int32_t* offsets, int32_t* token_of_row,
+                   int32_t* row_of_slot, void* stream);
+
+/* E4M3 rows with one fp32 scale per 128 consecutive elements:
+ *   s = max|block| / 448 (rounded once; at least 2^-126; 1 for a block of zeros),
+ *   code = the E4M3 value nearest to x / s, ties to the even code.
+ * A block that holds a NaN or an infinity gets the scale NaN and codes 0.
+ * x [*, ld] of `dtype`, K columns (a multiple of 16; the last block may be
+ * short), rows 16-byte aligned; codes [rows, K] uint8; scales
+ * [ceil(K / 128), ld_s], row r's in column r (ld_s >= rows).
+ * token_of_row (NULL: row r from row r): row r comes from row token_of_row[r] of
+ * the src_rows rows of x; an entry outside them leaves row r as it was.
+ * n_rows (NULL: all): device int32; rows at or behind it are left as they were. */
+int moe_quantize_rows_fp8(int rows, int K, const void* x, int dtype, long long ld, int src_rows,
+                          const int32_t* token_of_row, const int32_t* n_rows, uint8_t* codes, float* scales,
+                          long long ld_s, void* stream);
+
+/* E4M3 weights with one fp32 scale per 128 x 128 block, as above: w [G, N, K]
+ * bf16, K a multiple of 16; codes [G, N, K]; scales [G, ceil(N / 128),
+ * ceil(K / 128)].  The blocks of a group start at its first row.
+ * G and ceil(N / 128) at most 65535. */
+int moe_quantize_weights_fp8(int G, int N, int K, const moe_bf16* w, uint8_t* codes, float* scales, void* stream);
+
+typedef struct moe_glu_config {
+  int activation;        /* moe_activation                                              */
+  float gate_clamp_max;  /* SwiGLU: as in moe_config (+INF = off)                       */
+  float up_clamp;        /* SwiGLU: as in moe_config (>= 0; +INF = off)                 */
+  float situ_beta_gate;  /* SiTU-GLU (> 0, finite)                                      */
+  float situ_beta_up;    /* SiTU-GLU (> 0, finite)                                      */
+} moe_glu_config;
+
+/* The gated unit h of rows [gate | up] (gu [rows, ld], 2 I columns used),
+ * quantised from its fp32 value: codes [rows, I], scales [ceil(I / 128), ld_s].
+ * I a multiple of 16; n_rows as above. */
+int moe_glu_quantize_fp8(const moe_glu_config* cfg, int rows, int I, const moe_bf16* gu, long long ld,
+                         const int32_t* n_rows, uint8_t* codes, float* scales, long long ld_s, void* stream);
+
+/* The gradient of gu from dh [rows, ld_dh], that of h, quantised from its fp32
+ * value: codes [rows, 2 I], scales [2 I / 128, ld_s]; I a multiple of 128.  A
+ * clamped gate or up value has none, one at its bound has. */
+int moe_glu_backward_quantize_fp8(const moe_glu_config* cfg, int rows, int I, const moe_bf16* gu, long long ld,
+                                  const moe_bf16* dh, long long ld_dh, const int32_t* n_rows, uint8_t* codes,
+                                  float* scales, long long ld_s, void* stream);
+
+/* Products of E4M3 matrices whose scales are fp32, one per 128 elements of a row
+ * of a (a_scale [blocks, ld_as]) and per 128 x 128 block of the weights w [G, N, K]
+ * (w_scale [G, ceil(N / 128), ceil(K / 128)]):
+ *   transposed = 0   out[m, n] = sum over k of a[m, k] w[g, n, k],   a [M, K], out [M, N]
+ *   transposed = 1   out[m, k] = sum over n of a[m, n] w[g, n, k],   a [M, N], out [M, K]
+ * each code times its scale.  Rows offsets[g] .. offsets[g + 1] - 1 (device int32
+ * [G + 1], ascending, within 0 .. M; NULL: G = 1 and all M rows) meet group g;
+ * rows outside all groups are left as they were.  A block of 128 products is
+ * summed on the tensor core, blocks are added in fp32 in order as
+ * fma(block sum, a_scale * w_scale, sum), and the sum is rounded once to
+ * out_dtype (moe_dtype).  out [M, ldo].
+ * Limits: K a multiple of 16, and N too when transposed; G <= 1024;
+ * M, N, K < 2^31 - 256.  out may start and step at any alignment of its type
+ * (16-byte aligned rows store faster). */
+int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, int K, const uint8_t* a,
+                   const float* a_scale, long long ld_as, const uint8_t* w, const float* w_scale, void* out,
+                   int out_dtype, long long ldo, void* stream);
+
+/* out[t] = addend[t] + sum over slots j of w[t, j] y[row_of_slot[t, j]], fp32, the
+ * addend first, slots in order, rounded once to out_dtype.  y [rows, ld_y] of
+ * y_dtype, rows 16-byte aligned; w [T, k] or NULL (every slot 1); addend [T, D]
+ * bf16 or NULL; out [T, D].  A slot whose row is outside [0, rows) adds nothing.
+ * D a multiple of 8, k <= 32. */
+int moe_combine_rows(int T, int k, int D, int rows, const void* y, int y_dtype, long long ld_y,
+                     const int32_t* row_of_slot, const float* w, const moe_bf16* addend, void* out, int out_dtype,
+                     void* stream);
+
+/* Its gradients from dout [T, D] bf16: dy[row_of_slot[t, j]] = w[t, j] dout[t]
+ * (type and pitch of y; rows no slot names are left as they were) and
+ * dw[t, j] = <dout[t], y[row_of_slot[t, j]]> (NULL: not wanted, y may be NULL; 0
+ * for a slot without a row).  Slots name different rows. */
+int moe_combine_rows_backward(int T, int k, int D, int rows, const moe_bf16* dout, const void* y, int y_dtype,
+                              long long ld_y, const int32_t* row_of_slot, const float* w, void* dy, float* dw,
+                              void* stream);
+
+/* Read and clear the current device's error word of moe_matmul_fp8: MOE_OK;
+ * MOE_ETIMEOUT when a bounded device wait gave up (its output is incomplete);
+ * MOE_ECUDA when the copy failed or the word holds a value no kernel writes.
+ * Synchronises `stream`; not to be called while it is being captured. */
+int moe_get_operator_error(void* stream);
+
 int moe_destroy(moe_handle* h);
 const char* moe_status_string(int status);
 
