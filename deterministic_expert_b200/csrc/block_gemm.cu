@@ -35,6 +35,7 @@
 // CTA's copies and MMAs drain (bounded) and TMEM is freed.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "moe_internal.h"
@@ -46,25 +47,30 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 384;
 constexpr int kEpiW = 8;                       // epilogue warps
-constexpr int kRing = 184 * 1024;              // stage ring
+constexpr int kRing = 168 * 1024;              // stage ring
 constexpr int kRingMost = 12;
 constexpr int kWSlot = 128 * 128;              // weight bytes of a CTA's stage
 constexpr int kEpiSlot = 4096;                 // per epilogue warp
 constexpr int kBarSpace = 512;
-constexpr int kSmem = 1024 + kRing + kBarSpace + kEpiW * kEpiSlot;
+constexpr int kDoneBar = 2 * kRingMost + 4;  // index of the barrier of the last MMAs
+constexpr int kSlotBlocks = 4;                 // blocks whose scales a slot holds
+constexpr int kScaleSlots = 4;
+constexpr int kSlotBytes = kSlotBlocks * 256 * 4;
 constexpr uint32_t kCols = 512;
-constexpr uint32_t kBufCols = 256;
+constexpr int kSwapRows = 128;                 // tiles of at most this many rows have the weights as M
 constexpr unsigned long long kDrain = 200ull * 1000 * 1000;   // 200 ms
-constexpr int kAhead = 4;                      // blocks whose scales are loaded ahead
+constexpr int kSmem = 1024 + kRing + kBarSpace + kEpiW * kEpiSlot + kScaleSlots * kSlotBytes;
 
-// 184 KB ring: 5 stages of 32 KB, or 9 to 10 when a tile has few rows.
+// 168 KB ring: 5 stages of 32 KB, or up to 9 when a tile has few rows.
 static_assert(kRing / (kWSlot + 16 * 128) <= kRingMost, "stages");
+static_assert(kSlotBlocks == 4, "the epilogue reads a row's scales of a slot as one float4");
 
 // Error word of the handle-free operators on this device.
 __device__ int g_operator_error;
 
 struct BTile {
-  int g, row0, rows, n0, nt;   // group, first row, valid rows, first weight row / column, N of a swapped tile
+  int g, row0, rows, n0, nt;   // group, first row, valid rows, first output column, N of the MMA
+  int batch;                   // blocks of the contraction in one accumulator buffer
   bool swap;
 };
 
@@ -89,9 +95,34 @@ __device__ __forceinline__ BTile decode(const BlockGemmArgs& a, const int* start
   ti.n0 = (local - m * ntn) * 256;
   ti.row0 = r0 + m * a.tile_rows;
   ti.rows = min(a.tile_rows, r1 - ti.row0);
-  ti.swap = ti.rows < 256;
-  ti.nt = (ti.rows + 15) & ~15;
+  ti.swap = ti.rows <= kSwapRows;
+  ti.nt = ti.swap ? (ti.rows + 15) & ~15 : 256;
+  // Two buffers of 256 TMEM columns; tiles with few rows put several blocks in one,
+  // since handing a buffer over costs the epilogue about 800 cycles however few its
+  // columns (wait, load latency beside the running products, release).
+  ti.batch = ti.nt <= 64 ? 4 : (ti.nt <= 128 ? 2 : 1);
   return ti;
+}
+
+// Index of the smallest A box (16 << index rows) that holds `rows`.
+__device__ __forceinline__ int box_of(int rows) { return rows <= 16 ? 0 : (rows <= 32 ? 1 : (rows <= 64 ? 2 : 3)); }
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// Arrive once at `bar` in both CTAs when the pair's MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* map, int x, int y, int z, uint32_t bar) {
@@ -102,19 +133,59 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const void* map, int
       : "memory");
 }
 
-// A tile whose contiguous 128 bytes run along M or N (the transposed weights): one
-// 128-byte swizzle atom spans the operand's 128 rows, 8 contraction rows are 1024
-// bytes, an MMA's 32 contraction rows four of those.  Fields as in
-// sw128_kmajor_desc; the leading offset is between repeats along M or N, of which
-// there is one.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(16384u >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// High word of both operands' shared-memory descriptors (128-byte swizzle,
+// version 1, 1024 bytes between groups of 8): as sw128_kmajor_desc.  The transposed
+// weights are a tile whose contiguous 128 bytes run along M or N: one swizzle atom
+// spans the operand's 128 rows, 8 contraction rows are 1024 bytes, an MMA's 32
+// contraction rows 4096; the leading offset is between repeats along M or N, of
+// which there is one.
+constexpr uint64_t kDescHi = (1024u >> 4) | 1u << 14 | 2u << 29;
+
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Wait for the loads from TMEM; v is only defined after it, so it passes through.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                 "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                 "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                 "+r"(v[30]), "+r"(v[31])
+               :
+               : "memory");
+}
+
+// CH consecutive columns of this thread's TMEM lane, and the wait for them.
+template <int CH>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[CH]) {
+  if constexpr (CH == 32) {
+    tmem_ld32(taddr, r);
+  } else {
+    static_assert(CH == 8, "8 or 32 columns");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  }
+}
+template <int CH>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[CH]) {
+  if constexpr (CH == 32) {
+    tmem_wait32(v);
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+                 :
+                 : "memory");
+  }
 }
 
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -137,6 +208,65 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t p, uint64_t s) {
   asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(p), "l"(s));
 }
 
+// Barriers and shared memory by 32-bit shared addresses: the epilogue's threads
+// have no registers to spare for generic pointers.
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ int ld_shared_i32(uint32_t p) {
+  int v;
+  asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_shared_f32(uint32_t p) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(p));
+  return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t p, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(p), "f"(v) : "memory");
+}
+// One float by asynchronous copy, or a zero (nothing is read) unless `live`.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(p));
+  return v;
+}
+// Four floats as two packed pairs.
+__device__ __forceinline__ void ld_shared_pairs(uint32_t p, uint64_t& lo, uint64_t& hi) {
+  asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(lo), "=l"(hi) : "r"(p));
+}
+
+// A bounded wait: every failed try sleeps in hardware for up to about a
+// microsecond, so the limit is of the order of seconds.  On time-out it raises the
+// CTA's abort flag and the device's error word; it gives up at once when another
+// role has.
+constexpr int kTries = 4 << 20;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+  if (bar_try(bar, parity)) return true;
+  for (int i = 0; i < kTries; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if (ld_shared_i32(abort) != 0) return false;
+  }
+  asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(abort) : "memory");
+  atomicExch(&g_operator_error, kDevTimeout);
+  return false;
+}
+
 template <int TRANS, typename Out>
 __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constant__ BlockGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -145,37 +275,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
   const int S = min(kRingMost, kRing / (kWSlot + a.a_slot));
   uint8_t* sW = smem;                       // S x kWSlot
   uint8_t* sA = smem + S * kWSlot;          // S x a_slot
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing);
-  uint64_t* full = bars;
-  uint64_t* empty = bars + kRingMost;
-  uint64_t* tfull = bars + 2 * kRingMost;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* tdone = tempty + 2;
-  uint8_t* epi = smem + kRing + kBarSpace;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ int s_start[kMatmulMaxGroups + 1];
+  const uint32_t smem0 = smem_u32(smem);
+  const uint32_t full = smem0 + kRing, empty = full + 8 * kRingMost;
+  const uint32_t tfull = empty + 8 * kRingMost, tempty = tfull + 8 * 2, tdone = tempty + 8 * 2;
+  const uint32_t sfull = tdone + 8, sempty = sfull + 8 * kScaleSlots;
+  const uint32_t epi = smem0 + kRing + kBarSpace;
+  const uint32_t scales = epi + kEpiW * kEpiSlot;   // kScaleSlots x kSlotBytes
+  const uint32_t abort = smem_u32(&abort_flag);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kRing);
+    for (int s = 0; s < 2 * kRingMost; ++s) mbar_init(&bars[s], 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars[2 * kRingMost + b], 1);
+      mbar_init(&bars[2 * kRingMost + 2 + b], 2 * kEpiW);
     }
-    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 2 * kEpiW); }
-    mbar_init(tdone, 1);
+    mbar_init(&bars[kDoneBar], 1);
+    for (int i = 0; i < kScaleSlots; ++i) {
+      mbar_init(&bars[kDoneBar + 1 + i], 4);   // both CTAs' scale warps
+      mbar_init(&bars[kDoneBar + 1 + kScaleSlots + i], kEpiW);
+    }
     abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc_pair(&tmem_slot, kCols);
+  if (threadIdx.x == 0) {
+    prefetch_map(&a.mapA[box_of(a.tile_rows >= 256 ? 128 : a.tile_rows / 2)]);
+    prefetch_map(&a.mapW);
+  }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
-  volatile int* abort = &abort_flag;
-  int* err = &g_operator_error;
   griddep_wait();
   griddep_launch();
 
@@ -205,14 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
   __syncthreads();
   const int total = s_start[a.G];
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const uint32_t full0 = mapa_shared(full, 0);
-  const uint32_t tempty0 = mapa_shared(tempty, 0);
 
   if (warp < 4) {
-    // 64 + 2 x 216 registers of the 3 x 168 a thread that the block was launched with.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // 72 + 2 x 216 registers of the 3 x 168 a thread that the block was launched with.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- TMA producer
+      const uint32_t full0 = mapa_u32(full, 0);
       int stage = 0;
       uint32_t phase = 0;
       uint32_t issued = 0, issued_phase = 0;   // stages with a copy in flight, and its parity
@@ -220,21 +356,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       for (int t = pair; ok && t < total; t += pairs) {
         const BTile ti = decode(a, s_start, ntn, t);
         const int a_rows = ti.swap ? ti.nt / 2 : 128;
-        const int box = a_rows <= 16 ? 0 : (a_rows <= 32 ? 1 : (a_rows <= 64 ? 2 : 3));
+        const int box = box_of(a_rows);
         const int y = ti.row0 + static_cast<int>(rank) * a_rows;
         const int wr = ti.n0 + static_cast<int>(rank) * 128;
         const uint32_t bytes = (16u << box) * 128u;
         // The host sizes the A slot for tile_rows rows; a larger box would overrun it.
         if (static_cast<int>(bytes) > a.a_slot) {
-          atomicExch(err, kDevBadIndex);
-          *abort = 1;
+          atomicExch(&g_operator_error, kDevBadIndex);
+          abort_flag = 1;
           ok = false;
           break;
         }
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, abort, err, a.timeout_ns)) { ok = false; break; }
+          if (!bar_wait(empty + 8 * stage, phase ^ 1u, abort)) { ok = false; break; }
           // The even CTA counts both CTAs' bytes.
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (bytes + kWSlot));
+          if (leader)
+            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * stage),
+                         "r"(2 * (bytes + kWSlot)) : "memory");
           const uint32_t fb = full0 + 8 * stage;
           tma_load_2d_pair(sA + stage * a.a_slot, &a.mapA[box], kb * 128, y, fb);
           if (TRANS) tma_load_3d_pair(sW + stage * kWSlot, &a.mapW, wr, kb * 128, ti.g, fb);
@@ -246,133 +384,250 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       }
       if (!ok && leader)
         for (int s = 0; s < S; ++s)
-          if (issued >> s & 1u) mbar_wait_drain(&full[s], issued_phase >> s & 1u, kDrain);
-    } else if (warp == 1 && lane == 0 && leader) {
+          if (issued >> s & 1u) mbar_wait_drain(reinterpret_cast<uint64_t*>(smem + kRing) + s, issued_phase >> s & 1u, kDrain);
+    } else if (warp == 1 && leader) {
       // ------------------------------------------------------ MMA issuer
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, bphase = 0;
+      // The whole warp walks the loop (its addresses stay in uniform registers); one
+      // lane issues.
+      const bool issuer = elect_one();
+      int stage = 0, buf = 0, slot = 0;
+      uint32_t phase = 0, bphase = 0, sphase = 0;
+      // Low words of the operands' descriptors: start address and leading offset, >> 4.
+      const uint32_t tok_lo = (((smem0 + S * kWSlot) >> 4) & 0x3FFFu) | 1u << 16;
+      const uint32_t w_lo = ((smem0 >> 4) & 0x3FFFu) | (TRANS ? 16384u >> 4 : 1u) << 16;
+      const uint32_t tok_step = static_cast<uint32_t>(a.a_slot) >> 4;
       bool ok = true;
       for (int t = pair; ok && t < total; t += pairs) {
         const BTile ti = decode(a, s_start, ntn, t);
         // The transposed weights run along M (swapped: bit 15) or N (bit 16).
-        const uint32_t idesc = idesc_e4m3_f32(256, ti.swap ? ti.nt : 256) |
-                               (TRANS ? (ti.swap ? 1u << 15 : 1u << 16) : 0u);
+        const uint32_t idesc = idesc_e4m3_f32(256, ti.nt) | (TRANS ? (ti.swap ? 1u << 15 : 1u << 16) : 0u);
+        int left = 0;   // blocks that the current buffer still takes
+        uint32_t d = 0;
         for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&tempty[buf], bphase ^ 1u, abort, err, a.timeout_ns)) { ok = false; break; }
-          if (!mbar_wait(&full[stage], phase, abort, err, a.timeout_ns)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t ta = smem_u32(sA + stage * a.a_slot), wa = smem_u32(sW + stage * kWSlot);
-          const uint32_t d = tmem_base + buf * kBufCols;
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t td = sw128_kmajor_desc(ta + kk * 32);
-            const uint64_t wd = TRANS ? sw128_mnmajor_desc(wa + kk * 4096) : sw128_kmajor_desc(wa + kk * 32);
-            umma_e4m3_pair(d, ti.swap ? wd : td, ti.swap ? td : wd, idesc, kk != 0 ? 1u : 0u);
+          ok = bar_wait(full + 8 * stage, phase, abort);
+          if (kb % kSlotBlocks == 0) {
+            // The scales of these blocks are there before their products are begun, so
+            // the epilogue, which waits for the products, need not wait for them too.
+            ok = ok && bar_wait(sfull + 8 * slot, sphase, abort);
+            if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
           }
-          umma_commit_pair_mc(&empty[stage], 0x3);
-          umma_commit_pair_mc(&tfull[buf], 0x3);
+          if (left == 0) {
+            ok = ok && bar_wait(tempty + 8 * buf, bphase ^ 1u, abort);
+            left = ti.batch;
+            d = tmem_base + buf * 256;
+          }
+          if (!__all_sync(kFull, ok)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t tlo = tok_lo + stage * tok_step, wlo = w_lo + stage * (kWSlot >> 4);
+          const uint32_t alo = ti.swap ? wlo : tlo, blo = ti.swap ? tlo : wlo;
+          const uint32_t astep = TRANS && ti.swap ? 4096 >> 4 : 2, bstep = TRANS && !ti.swap ? 4096 >> 4 : 2;
+          --left;
+          const bool last = left == 0 || kb == nkb - 1;
+          if (issuer) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_e4m3_pair(d, (kDescHi << 32) | (alo + kk * astep), (kDescHi << 32) | (blo + kk * bstep), idesc,
+                             kk != 0 ? 1u : 0u);
+            if (last) commit_pair(tfull + 8 * buf);
+            commit_pair(empty + 8 * stage);
+          }
+          __syncwarp();
+          d += 256 / ti.batch;
           if (++stage == S) { stage = 0; phase ^= 1u; }
-          if (++buf == 2) { buf = 0; bphase ^= 1u; }
+          if (last) {
+            left = 0;
+            if (++buf == 2) { buf = 0; bphase ^= 1u; }
+          }
         }
       }
-      umma_commit_pair_mc(tdone, 0x1);
-      mbar_wait_drain(tdone, 0, kDrain);
+      if (issuer) {
+      uint64_t* done = reinterpret_cast<uint64_t*>(smem + kRing) + kDoneBar;
+      umma_commit_pair_mc(done, 0x1);
+      mbar_wait_drain(done, 0, kDrain);
+      }
+    } else if (warp >= 2) {
+      // ---------------------------------------------------- scale warps
+      // fl(sa sw) of kSlotBlocks blocks at a time, 256 numbers a block: full tiles
+      // the CTA's 128 rows under each of its two weight blocks (a row's numbers of
+      // the slot side by side), swapped tiles the tile's rows under the CTA's weight
+      // block.  The rows' factors come by 4-byte asynchronous copies (rows start at
+      // any address) two slots ahead; the thread that copied a number multiplies
+      // it.  A slot covers several blocks because every hand-over costs the
+      // epilogue's warps about 100 cycles, and their round trip with the tensor
+      // core is what bounds full tiles (one block a slot: 94 us where this takes
+      // 76, M = 9472, N = 1024, K = 7168).
+      const uint32_t sfull0 = mapa_u32(sfull, 0);
+      const int i0 = threadIdx.x - 64;
+      int slot = 0, fslot = 0;            // slot multiplied next, slot filled next
+      uint32_t fphase = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < total; t += pairs) {
+        const BTile ti = decode(a, s_start, ntn, t);
+        const int row = (ti.swap ? 0 : static_cast<int>(rank) * 128) + i0;
+        const float* ps = a.a_scale + ti.row0 + row;
+        const int ob = ti.n0 / 128 + (ti.swap ? static_cast<int>(rank) : 0);
+        const float* pw = a.w_scale + ti.g * a.ws_g + ob * a.ws_o;
+        // Blocks behind the last column are multiplied by 0 and not stored; rows
+        // behind the tile's last are not read.
+        const bool w0 = ob * 128 < a.width, w1 = !ti.swap && (ob + 1) * 128 < a.width;
+        const int nsl = (nkb + kSlotBlocks - 1) / kSlotBlocks;
+        // Cell of number i (rows i0 + 64 i, or i & 1 and weight block i >> 1) of block z.
+        auto cell = [&](int sl, int z, int i) {
+          return scales + sl * kSlotBytes +
+                 (ti.swap ? (z * 256 + i * 64 + i0) * 4 : ((i * 64 + i0) * kSlotBlocks + z) * 4);
+        };
+        auto fill = [&](int j) {
+          if (j < nsl) {
+            ok = ok && bar_wait(sempty + 8 * fslot, fphase ^ 1u, abort);
+            for (int z = 0; ok && z < kSlotBlocks && j * kSlotBlocks + z < nkb; ++z) {
+              const float* p = ps + static_cast<long long>(j * kSlotBlocks + z) * a.ld_as;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (ti.swap || i < 2) copy4(cell(fslot, z, i), p + 64 * i, row + 64 * i < ti.rows);
+            }
+            if (++fslot == kScaleSlots) { fslot = 0; fphase ^= 1u; }
+          }
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        fill(0);
+        fill(1);
+        for (int j = 0; j < nsl; ++j) {
+          float sw[kSlotBlocks][2];
+#pragma unroll
+          for (int z = 0; z < kSlotBlocks; ++z) {
+            const int kb = j * kSlotBlocks + z;
+            sw[z][0] = kb < nkb && w0 ? pw[kb * a.ws_c] : 0.f;
+            sw[z][1] = kb < nkb && w1 ? pw[kb * a.ws_c + a.ws_o] : 0.f;
+          }
+          fill(j + 2);
+          if (!__all_sync(kFull, ok)) { ok = false; break; }
+          asm volatile("cp.async.wait_group 2;" ::: "memory");
+#pragma unroll
+          for (int z = 0; z < kSlotBlocks; ++z) {
+            if (ti.swap) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t c = cell(slot, z, i);
+                st_shared_f32(c, __fmul_rn(ld_shared_f32(c), sw[z][0]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float v = ld_shared_f32(cell(slot, z, i));
+                st_shared_f32(cell(slot, z, i), __fmul_rn(v, sw[z][0]));
+                st_shared_f32(cell(slot, z, i + 2), __fmul_rn(v, sw[z][1]));
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(sfull0 + 8 * slot);
+          if (++slot == kScaleSlots) slot = 0;
+        }
+      }
+      // No copy is in flight when the CTA goes.
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // --------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - 4) >> 2;
-    uint8_t* stage_w = epi + (warp - 4) * kEpiSlot;
-    float* s_sc = reinterpret_cast<float*>(stage_w);   // swapped: two slots of 128 scales
-    int buf = 0;
+    const uint32_t tempty0 = mapa_u32(tempty, 0);
+    const uint32_t tlane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    int buf = 0, slot = 0;
     uint32_t bphase = 0;
     bool ok = true;
     for (int t = pair; ok && t < total; t += pairs) {
-      const BTile ti = decode(a, s_start, ntn, t);
-      const int hc = ti.nt >> 1;   // swapped: columns (rows of A) of this warp
-      // Scale addresses: the row of A this lane loads for (full tile: its own row;
-      // swapped: rows lane, lane + 32, ... of the warp's), the weights' block.
-      const int own = ti.swap ? half * hc + lane : static_cast<int>(rank) * 128 + q * 32 + lane;
-      const float* ps = a.a_scale + ti.row0 + own;
-      const int oblk = ti.n0 / 128 + (ti.swap ? static_cast<int>(rank) : half);
-      // Past the last block (its columns are not stored) the scale is taken as 0.
-      const bool wlive = oblk * 128 < a.width;
-      const float* pw = a.w_scale + ti.g * a.ws_g + (wlive ? oblk : 0) * a.ws_o;
-      // Rows behind the tile's last are never read (they may lie behind the buffer).
-      bool live[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        live[i] = own + 32 * i < ti.rows && (ti.swap ? lane + 32 * i < hc : i == 0);
-      float sa[kAhead][4], sw[kAhead];
-      auto load = [&](int slot, int kb) {
-        const bool in = kb < nkb;
-        sw[slot] = in && wlive ? pw[kb * a.ws_c] : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sa[slot][i] = in && live[i] ? ps[kb * a.ld_as + 32 * i] : 0.f;
-      };
-#pragma unroll
-      for (int z = 0; z < kAhead; ++z) load(z, z);
-
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      for (int kb = 0; kb < nkb; ++kb) {
-        ok = mbar_wait(&tfull[buf], bphase, abort, err, a.timeout_ns);
-        if (!__all_sync(kFull, ok)) { ok = false; break; }
+      auto wait_products = [&]() {
+        ok = bar_wait(tfull + 8 * buf, bphase, abort);
+        ok = __all_sync(kFull, ok);
         tc_fence_after();
-        const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * kBufCols;
-        if (!ti.swap) {
-          const float s = __fmul_rn(sa[0][0], sw[0]);
-          const uint64_t s2 = pack2(s, s);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tb + half * 128 + c * 32, v);
-            tmem_ld_wait();
-            if (c == 3) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], pack2u(v[2 * i], v[2 * i + 1]), s2);
-          }
-        } else {
-          float* sc = s_sc + (kb & 1) * 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i * 32 < hc) sc[i * 32 + lane] = __fmul_rn(sa[0][i], sw[0]);
-          __syncwarp();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 >= hc) continue;
-            uint32_t v[32];
-            tmem_ld32(tb + half * hc + c * 32, v);
-            tmem_ld_wait();
-            if ((c + 1) * 32 >= hc) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + c * 32 + 4 * i);
-              fma2(acc[c * 16 + 2 * i], pack2u(v[4 * i], v[4 * i + 1]), pack2(f.x, f.y));
-              fma2(acc[c * 16 + 2 * i + 1], pack2u(v[4 * i + 2], v[4 * i + 3]), pack2(f.z, f.w));
-            }
-          }
-        }
-        // Move the scales up by one block and load the one after the last.
-#pragma unroll
-        for (int z = 0; z + 1 < kAhead; ++z) {
-          sw[z] = sw[z + 1];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sa[z][i] = sa[z + 1][i];
-        }
-        load(kAhead - 1, kb + kAhead);
+        return ok;
+      };
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty0 + 8 * buf);
         if (++buf == 2) { buf = 0; bphase ^= 1u; }
+      };
+      auto give_scales = [&]() {
+        __syncwarp();
+        if (lane == 0) bar_arrive(sempty + 8 * slot);
+        if (++slot == kScaleSlots) slot = 0;
+      };
+      // Full tiles: one block a buffer, four chunks of 32 columns, the next one's load
+      // under the multiply-adds of the last; the buffer is given back as soon as the
+      // last chunk has arrived.
+      auto full_tile = [&]() {
+        float4 s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int kb = 0; kb < nkb; ++kb) {
+          const int z = kb % kSlotBlocks;
+          if (!wait_products()) return;
+          const uint32_t tb = tlane + buf * 256 + half * 128;
+          uint32_t v[2][32];
+          tmem_ld32(tb, v[0]);
+          if (z == 0) s4 = ld_shared_f32x4(scales + slot * kSlotBytes + (half * 128 + q * 32 + lane) * 16);
+          const uint64_t s2 = pack2(s4.x, s4.x);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_wait32(v[c & 1]);
+            if (c < 3) tmem_ld32(tb + (c + 1) * 32, v[(c + 1) & 1]);
+            else release();
+            const uint32_t(&x)[32] = v[c & 1];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], pack2u(x[2 * i], x[2 * i + 1]), s2);
+          }
+          s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
+          if (z == kSlotBlocks - 1 || kb == nkb - 1) give_scales();
+        }
+      };
+      // Swapped tiles: BATCH blocks a buffer; the 128 / BATCH columns that a warp can
+      // have of a block are loaded CH at a time, all blocks' at once.
+      auto swapped_tile = [&](auto batch, auto chunk, const int hc) {
+        constexpr int BATCH = decltype(batch)::value, CH = decltype(chunk)::value, N = 128 / BATCH / CH;
+        for (int kb = 0; kb < nkb; kb += BATCH) {
+          const int z = kb % kSlotBlocks;
+          if (!wait_products()) return;
+          const uint32_t tb = tlane + buf * 256 + half * hc;
+          const uint32_t sc = scales + slot * kSlotBytes + (z * 256 + half * hc) * 4;
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            if (c * CH >= hc) break;
+            uint32_t v[BATCH][CH];
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) tmem_ld<CH>(tb + j * (256 / BATCH) + c * CH, v[j]);
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) tmem_wait<CH>(v[j]);
+            if ((c + 1) * CH >= hc) release();
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) {
+              if (kb + j >= nkb) break;
+#pragma unroll
+              for (int i = 0; i < CH / 4; ++i) {
+                uint64_t lo, hi;
+                ld_shared_pairs(sc + (j * 256 + c * CH + 4 * i) * 4, lo, hi);
+                fma2(acc[c * (CH / 2) + 2 * i], pack2u(v[j][4 * i], v[j][4 * i + 1]), lo);
+                fma2(acc[c * (CH / 2) + 2 * i + 1], pack2u(v[j][4 * i + 2], v[j][4 * i + 3]), hi);
+              }
+            }
+          }
+          if (z + BATCH == kSlotBlocks || kb + BATCH >= nkb) give_scales();
+        }
+      };
+      {
+        const BTile ti = decode(a, s_start, ntn, t);
+        if (!ti.swap) full_tile();
+        else if (ti.batch == 4) swapped_tile(std::integral_constant<int, 4>{}, std::integral_constant<int, 8>{}, ti.nt >> 1);
+        else swapped_tile(std::integral_constant<int, 2>{}, std::integral_constant<int, 32>{}, ti.nt >> 1);
       }
       if (!ok) break;
+      // Decoded again rather than kept in registers over the loop.
+      asm volatile("" ::: "memory");
+      const BTile ti = decode(a, s_start, ntn, t);
+      const int hc = ti.nt >> 1;
+      uint8_t* stage_w = smem + kRing + kBarSpace + (warp - 4) * kEpiSlot;
 
       // ------------------------------------------------------- store
       Out* out = static_cast<Out*>(a.out);
@@ -410,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
             const int r = it * 4 + (lane >> 3), ch = lane & 7;
             const int col = col0 + p * kSeg + ch * kPer;
             const uint4 u = *reinterpret_cast<const uint4*>(stage_w + r * 128 + ((ch ^ (r & 7)) << 4));
-            Out* dst = out + static_cast<size_t>(ti.row0 + r0 + r) * a.ldo + col;   // 256 valid rows in a full tile
+            if (r0 + r >= ti.rows) continue;
+            Out* dst = out + static_cast<size_t>(ti.row0 + r0 + r) * a.ldo + col;
             if (a.out_vec && col + kPer <= a.width) {
               *reinterpret_cast<uint4*>(dst) = u;
             } else {
@@ -428,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         const int valid = min(hc, ti.rows - half * hc);
         Out* dst = out + static_cast<size_t>(ti.row0 + half * hc) * a.ldo + col;
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
+        for (int i = 0; i < kSwapRows / 4; ++i) {
           if (2 * i >= valid) break;
           const float2 f = unpack2(acc[i]);
           if (col < a.width) {

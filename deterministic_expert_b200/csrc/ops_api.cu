@@ -283,7 +283,6 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   g.ldo = ldo;
   g.out_f32 = out_dtype == MOE_DTYPE_F32;
   g.out_vec = al(out, 16) && pitch16(ldo, osize);
-  g.timeout_ns = 2000ull * 1000 * 1000;
   const long long max_tiles = ntn * ((M + tr - 1) / tr + G);
   return status(launch_block_gemm(g, static_cast<int>(std::min<long long>(max_tiles, pairs)),
                                   static_cast<cudaStream_t>(stream)));
