@@ -3,15 +3,17 @@
 //
 //   s = fp32(max|block| / 448), at least 2^-126; 1 for a block of zeros
 //   code = the E4M3 value nearest to x / s, ties to the even code
-// The quotient is rounded once: fp32 arithmetic decides every element whose
-// quotient is not within a few ulp of the middle of two codes, and the others are
-// settled by the exact sign of the division's remainder.  A block that holds a
+// The quotient is rounded once: an enclosure of it decides every element that is
+// not within 2^-20 of the middle of two codes, and the others are settled by the
+// exact sign of x - middle * s.  A block that holds a
 // NaN or an infinity gets the scale NaN and zero codes, so that products with it
 // are NaN.
 //
 // Sources of a row: bf16 or fp32 rows (optionally gathered: row r from row
 // token_of_row[r]), the experts' gated unit of a [gate | up] row (never stored:
 // the unit's fp32 value is quantised directly), or that unit's gradient.
+#include <algorithm>
+
 #include "common.cuh"
 #include "moe_internal.h"
 #include "ops_internal.h"
@@ -23,53 +25,34 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBlk = 128;
 constexpr float kE4m3Max = 448.f;
 
+// A block's scale and two reciprocals of it, one a little too small and one a
+// little too large: x * lo and x * hi enclose x / s (the reciprocal is within an
+// ulp, each product rounds by half of one: 2^-20 covers all of it four times).
 struct BlockScale {
-  float s, inv;
+  float s, inv, lo, hi;
+  float rem;   // amax - 448 s, exact (0 for a raised scale, whose division is by a power of two)
 };
 
 // amax is the block's maximum magnitude, NaN or infinite if an element is.
+// amax / 448: an estimate plus its exact remainder times the reciprocal, rounded
+// once.  448 = 7 * 64, so the quotient is at least 1/14 ulp away from the middle of
+// two fp32 values, far more than the 2^-46 that the sum is off: it is the
+// correctly rounded quotient.
 __device__ __forceinline__ BlockScale block_scale(float amax) {
+  constexpr float kInv448 = 1.f / 448.f;
+  const float q = amax * kInv448;
   BlockScale b;
+  b.s = fmaf(fmaf(-q, kE4m3Max, amax), kInv448, q);
+  b.rem = b.s >= 1.17549435e-38f ? fmaf(-b.s, kE4m3Max, amax) : 0.f;
+  b.s = amax > 0.f ? fmaxf(b.s, 1.17549435e-38f) : 1.f;
+  b.inv = __fdividef(1.f, b.s);
   if (!(amax < INFINITY)) {
     b.s = __int_as_float(0x7fffffff);
     b.inv = 0.f;
-    return b;
   }
-  b.s = amax > 0.f ? fmaxf(__fdiv_rn(amax, kE4m3Max), 1.17549435e-38f) : 1.f;
-  b.inv = __frcp_rn(b.s);
+  b.lo = b.inv * (1.f - 0x1p-20f);
+  b.hi = b.inv * (1.f + 0x1p-20f);
   return b;
-}
-
-// The quotient x / s, moved off the middle of two codes to the side where the
-// exact quotient lies.  q is the correctly rounded quotient, on the exact one's
-// side of every fp32 value except itself; middles of codes have 19 zero bits, and
-// there the remainder x - q s (exact in one fused operation, after both are
-// scaled by a power of two so that it cannot underflow) tells the side.
-__device__ __noinline__ float quotient_exact(float x, float s) {
-  const float f = __int_as_float(0x7f000000 - (__float_as_int(s) & 0x7f800000));   // 2^-floor(log2 s)
-  s *= f;
-  x *= f;
-  float q = __fdiv_rn(x, s);
-  if ((__float_as_uint(q) & 0x7FFFFu) == 0 && q != 0.f) {
-    const float r = fmaf(-q, s, x);
-    if (r != 0.f) {
-      const bool away = (r > 0.f) == (q > 0.f);   // the exact quotient is larger in magnitude
-      q = __int_as_float(__float_as_int(q) + (away ? 1 : -1));
-    }
-  }
-  return q;
-}
-
-// x * inv is within two ulp of x / s.  Codes have 3 mantissa bits, so the middle
-// of two normal codes has fp32 mantissa bits 1000...0 below them (20 low bits);
-// below 2^-6 the codes are multiples of 2^-9, which adding 2^-6 brings to the same
-// bits.  Anything within 4 ulp of a middle takes the exact way.
-__device__ __forceinline__ float code_quotient(float x, const BlockScale& b) {
-  const float q = __fmul_rn(x, b.inv);
-  float y = fabsf(q);
-  if (y < 0.015625f) y += 0.015625f;
-  const uint32_t d = (__float_as_uint(y) - 0x80000u + 4u) & 0xFFFFFu;
-  return d <= 8u ? quotient_exact(x, b.s) : q;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -78,12 +61,99 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], const BlockScale& b) {
-  if (b.inv == 0.f) return make_uint2(0, 0);   // scale NaN: zero codes
-  float q[8];
+// Of the two neighbouring codes that enclose x / s (c and the next in magnitude)
+// the nearest, the even one for a tie.  near is within 2^-19 of the middle m of the
+// two, so m is near with its bits below half a code's step cut off: codes have 3
+// mantissa bits, and those below 2^-6 are multiples of 2^-9, which adding 2^-6
+// brings to the same bits.  x - m s is exact in sign in one fused operation, once
+// a tiny s and x are scaled up.
+__device__ __forceinline__ uint32_t nearest_code(float x, float s, float near, uint32_t c) {
+  const float low = near < 0.015625f ? 0.015625f : 0.f;
+  const float m = __uint_as_float((__float_as_uint(near + low) & 0xFFF00000u) | 0x80000u) - low;
+  const float up = s < 0x1p-60f ? 0x1p64f : 1.f;
+  const float r = fmaf(-m, s * up, fabsf(x) * up);
+  return c + ((r > 0.f || (r == 0.f && (c & 1u))) ? 1u : 0u);
+}
+
+// Pairs of fp32 in one operation.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint64_t p) {
+  float x, y;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+  return e4m3x2(x, y);
+}
+
+// Codes of eight elements that are bf16 values, in a block whose maximum is one.
+// With 8-bit significands a (x) and b (amax), 448 x / amax is 7 a / b times a power
+// of two; it is either the middle of two codes exactly, or (numerator and
+// denominator are integers, the middles' significands have 5 bits) at least 2^-13
+// of its size away.  So x / s lies beside a middle only where 448 x / amax is one,
+// and then on the side that the rounding of s to fp32 went away from: a
+// reciprocal 2^-18 too small (s rounded up) or too large (down) takes every such
+// element to its side and no other across.  Where s = amax / 448 exactly, the
+// quotient is corrected by its exact remainder, so that middles are met exactly and
+// go to the even code.
+__device__ __forceinline__ uint2 codes8_bf16(const float (&v)[8], const BlockScale& b) {
+  const float f = b.rem == 0.f ? b.inv : b.inv * (b.rem < 0.f ? 1.f - 0x1p-18f : 1.f + 0x1p-18f);
+  const uint64_t f2 = pair(f, f);
+  uint64_t x[4], q[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = code_quotient(v[i], b);
-  return make_uint2(e4m3x2(q[0], q[1]) | (e4m3x2(q[2], q[3]) << 16), e4m3x2(q[4], q[5]) | (e4m3x2(q[6], q[7]) << 16));
+  for (int i = 0; i < 4; ++i) {
+    x[i] = pair(v[2 * i], v[2 * i + 1]);
+    q[i] = mul2(x[i], f2);
+  }
+  uint2 c = make_uint2(e4m3x2(q[0]) | e4m3x2(q[1]) << 16, e4m3x2(q[2]) | e4m3x2(q[3]) << 16);
+  if (b.rem == 0.f) {
+    const uint64_t s2 = pair(-b.s, -b.s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = fma2(fma2(q[i], s2, x[i]), f2, q[i]);
+    // (The correction of a zero is a zero of either sign: signs stay.)
+    c.x = (c.x & 0x80808080u) | e4m3x2(q[0]) | e4m3x2(q[1]) << 16;
+    c.y = (c.y & 0x80808080u) | e4m3x2(q[2]) | e4m3x2(q[3]) << 16;
+  }
+  return c;
+}
+
+// Codes of eight fp32 elements.  Rounding is monotone, so where both ends of the
+// enclosure have one code, that is the quotient's: a product and half a conversion
+// of each end an element.  The others (about one in 50000) are settled one by one.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], const BlockScale& b) {
+  const uint64_t l2 = pair(b.lo, b.lo), h2 = pair(b.hi, b.hi);
+  uint32_t lo[2], hi[2];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const uint64_t p = pair(v[4 * w], v[4 * w + 1]), q = pair(v[4 * w + 2], v[4 * w + 3]);
+    lo[w] = e4m3x2(mul2(p, l2)) | e4m3x2(mul2(q, l2)) << 16;
+    hi[w] = e4m3x2(mul2(p, h2)) | e4m3x2(mul2(q, h2)) << 16;
+  }
+  if (lo[0] != hi[0] || lo[1] != hi[1]) {
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      uint32_t diff = lo[w] ^ hi[w];
+      while (diff != 0) {
+        const int i = (__ffs(diff) - 1) >> 3;
+        const float x = i == 0 ? v[4 * w] : (i == 1 ? v[4 * w + 1] : (i == 2 ? v[4 * w + 2] : v[4 * w + 3]));
+        const uint32_t c = lo[w] >> (8 * i) & 0xFFu;
+        lo[w] += (nearest_code(x, b.s, fabsf(x) * b.hi, c) - c) << (8 * i);   // the next code at most: no carry
+        diff &= ~(0xFFu << (8 * i));
+      }
+    }
+  }
+  return make_uint2(lo[0], lo[1]);
 }
 
 // Maximum magnitude with NaN kept (as a bit pattern above infinity's).
@@ -93,9 +163,17 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
   return m;
 }
-__device__ __forceinline__ float half_warp_max(uint32_t m) {
+// The same of eight packed bf16 values, as an fp32 bit pattern.
+__device__ __forceinline__ uint32_t amax8(const uint4& u) {
+  const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(&u);
+  const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&m) & 0x7fff7fffu;
+  return max(w & 0xffff0000u, w << 16);
+}
+// Over the eight lanes of a block.
+__device__ __forceinline__ float lanes_max(uint32_t m) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+  for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
   return __uint_as_float(m);
 }
 
@@ -108,54 +186,70 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   }
 }
 
-// The gated unit and its derivatives in fp32 (expf and the approximate division,
-// about 3 ulp: the code's rounding is 2^-4).
+// sigmoid(g) = 1 / (1 + 2^(-g log2 e)): the exponent's rounding is |g| 2^-24 of the
+// power's size, the two approximations an ulp or two.
+__device__ __forceinline__ float sigmoid_approx(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));   // e infinite: 0
+  return r;
+}
+
+// The gated unit and its derivatives in fp32 (the code's rounding is 2^-4):
 //   SwiGLU    h = a(g) b(u), a = silu(min(g, cg)), b = clamp(u, -cu, cu)
 //   SiTU-GLU  a = bg tanh(g / bg) sigmoid(g), b = bu tanh(u / bu)
-// sigma = 1 / (1 + e), 1 - sigma = e sigma with e = e^-g held finite so
-// that neither product meets infinity times zero.
-__device__ __forceinline__ void glu_parts(float g, float u, const QuantArgs& a, bool grad, float& av, float& bv,
-                                          float& da, float& db) {
-  if (a.act == MOE_ACT_SITU_GLU) {
-    const float e = expf(fminf(-g, 88.f));
-    const float sg = __fdividef(1.f, 1.f + e);
+// A NaN stays one; a clamped value has no gradient, one at its bound has.
+enum GluKind : int { kSwiglu = 0, kSwigluClamped = 1, kSitu = 2 };
+
+template <int GLU, bool GRAD>
+__device__ __forceinline__ void glu_parts(float g, float u, const QuantArgs& a, float& av, float& bv, float& da,
+                                          float& db) {
+  if (GLU == kSitu) {
+    const float sg = sigmoid_approx(g);
     const float tg = tanhf(__fdiv_rn(g, a.beta_g)), tu = tanhf(__fdiv_rn(u, a.beta_u));
     av = a.beta_g * tg * sg;
     bv = a.beta_u * tu;
-    if (grad) {
-      da = (1.f - tg * tg) * sg + a.beta_g * tg * sg * (e * sg);
+    if (GRAD) {
+      da = fmaf(1.f - tg * tg, sg, av * (1.f - sg));
       db = 1.f - tu * tu;
     }
   } else {
-    const float gc = fminf(g, a.gate_clamp);
-    const float e = expf(fminf(-gc, 88.f));
-    const float sg = __fdividef(1.f, 1.f + e);
-    av = gc * sg;
-    bv = fminf(fmaxf(u, -a.up_clamp), a.up_clamp);
-    if (grad) {
-      // A clamped value has no gradient; one at its bound has.
-      da = g <= a.gate_clamp ? sg * (1.f + gc * (e * sg)) : 0.f;
-      db = (u >= -a.up_clamp && u <= a.up_clamp) ? 1.f : 0.f;
+    float pass = 1.f;
+    db = 1.f;
+    bv = u;
+    if (GLU == kSwigluClamped) {
+      pass = g > a.gate_clamp ? 0.f : 1.f;
+      g = g > a.gate_clamp ? a.gate_clamp : g;
+      db = (u > a.up_clamp || u < -a.up_clamp) ? 0.f : 1.f;
+      bv = u > a.up_clamp ? a.up_clamp : (u < -a.up_clamp ? -a.up_clamp : u);
+    }
+    const float sg = sigmoid_approx(g);
+    av = g * sg;
+    if (GRAD) {
+      da = sg * fmaf(g, 1.f - sg, 1.f);
+      if (GLU == kSwigluClamped) da *= pass;
     }
   }
-  // fminf and fmaxf drop a NaN: keep it.
-  if (isnan(g)) av = da = g;
-  if (isnan(u)) bv = db = u;
 }
 
-// Block of 256 threads = 16 half-warps, each on one row; a half-warp takes a
-// block of 128 columns (8 a lane, one 16-byte load of bf16), kUnroll of them at a
-// time so that their loads are in flight together.
+// Eight lanes take a block of 128 columns: lane i its columns 8 i .. 8 i + 7 and
+// 64 + 8 i .. 64 + 8 i + 7, so that its scale costs each lane a sixteenth of a
+// block and every load and store of the eight lanes is one segment.  A CTA of 256
+// threads takes 32 rows (their scales of a block are one 128-byte segment) and
+// walks their blocks, U at a time so that their loads are in flight together.
 // Bound by memory: every element is read once and its code written once.
-constexpr int kRowsPerCta = 16;
-constexpr int kUnroll = 2;
-
+constexpr int kRowsPerCta = 32;
 template <int KIND>
+constexpr int kUnroll = KIND == kQuantBf16 ? 2 : 1;
+
+template <int KIND, int GLU = kSwiglu>
 __global__ void __launch_bounds__(256) k_quant_blocks(const QuantArgs a) {
+  constexpr int U = kUnroll<KIND>;
+  constexpr bool GRAD = KIND == kQuantGluBackward;
   griddep_wait();
   griddep_launch();
-  const int r = blockIdx.x * kRowsPerCta + (threadIdx.x >> 4);
-  const int hl = threadIdx.x & 15;
+  const int r = blockIdx.x * kRowsPerCta + (threadIdx.x >> 3);
+  const int l = threadIdx.x & 7;
   int limit = a.R;
   if (a.n_rows != nullptr) limit = min(limit, *a.n_rows);
   long long src = r;
@@ -165,86 +259,96 @@ __global__ void __launch_bounds__(256) k_quant_blocks(const QuantArgs a) {
     live = src >= 0 && src < a.src_rows;
   }
   const int nkb = (a.K + kBlk - 1) / kBlk;
-  const size_t row = static_cast<size_t>(src) * static_cast<size_t>(a.ld);
+  const size_t row = static_cast<size_t>(src) * static_cast<size_t>(a.ld) + l * 8;
+  const uint16_t* dh = GRAD ? a.dh + static_cast<size_t>(r) * a.ld_dh + l * 8 : nullptr;
+  uint8_t* codes = a.codes + static_cast<size_t>(r) * (GRAD ? 2 * a.K : a.K) + l * 8;
+  float* scales = a.scales + r;
   const int per_y = (nkb + gridDim.y - 1) / gridDim.y;
   const int kb1 = min(nkb, static_cast<int>(blockIdx.y + 1) * per_y);
-  for (int kb0 = blockIdx.y * per_y; kb0 < kb1; kb0 += kUnroll) {
-    float v[kUnroll][8];
-    float w[KIND == kQuantGluBackward ? kUnroll : 1][8];   // the up half's gradient
+  // Columns c .. c + 7 of the row exist (l * 8 is in the pointers).
+  auto in = [&](int c) { return live && c + l * 8 < a.K; };
+  // A block's codes and scale; `first`: columns before it in the written row.
+  auto put = [&](const float(&v)[2][8], uint32_t m, int c, int sb, int first) {
+    const BlockScale b = block_scale(lanes_max(m));
+    if (live) {
 #pragma unroll
-    for (int z = 0; z < kUnroll; ++z)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[z][i] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        uint2 q = KIND == kQuantBf16 ? codes8_bf16(v[h], b) : codes8(v[h], b);
+        if (b.inv == 0.f) q = make_uint2(0, 0);   // scale NaN: zero codes
+        if (in(c + 64 * h)) *reinterpret_cast<uint2*>(codes + first + c + 64 * h) = q;
+      }
+      if (l == 0) scales[sb * a.ld_s] = b.s;
+    }
+  };
+  for (int kb0 = blockIdx.y * per_y; kb0 < kb1; kb0 += U) {
     if constexpr (KIND == kQuantBf16) {
-      uint4 u[kUnroll];
+      uint4 u[U][2];
 #pragma unroll
-      for (int z = 0; z < kUnroll; ++z) {
-        const int c = (kb0 + z) * kBlk + hl * 8;
-        u[z] = make_uint4(0, 0, 0, 0);
-        if (live && kb0 + z < kb1 && c < a.K)
-          u[z] = *(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row + c));
+      for (int z = 0; z < U; ++z)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = (kb0 + z) * kBlk + 64 * h;
+          u[z][h] = make_uint4(0, 0, 0, 0);
+          if (kb0 + z < kb1 && in(c)) u[z][h] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + row + c);
+        }
+#pragma unroll
+      for (int z = 0; z < U; ++z) {
+        if (kb0 + z >= kb1) break;
+        float v[2][8];
+        unpack8(u[z][0], v[0]);
+        unpack8(u[z][1], v[1]);
+        put(v, max(amax8(u[z][0]), amax8(u[z][1])), (kb0 + z) * kBlk, kb0 + z, 0);
       }
-#pragma unroll
-      for (int z = 0; z < kUnroll; ++z) unpack8(u[z], v[z]);
     } else if constexpr (KIND == kQuantF32) {
+      float v[2][8];
 #pragma unroll
-      for (int z = 0; z < kUnroll; ++z) {
-        const int c = (kb0 + z) * kBlk + hl * 8;
-        if (live && kb0 + z < kb1 && c < a.K) {
+      for (int h = 0; h < 2; ++h) {
+        const int c = kb0 * kBlk + 64 * h;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        if (in(c)) {
           const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.x) + row + c);
-          const float4 lo = *(p), hi = *(p + 1);
-          v[z][0] = lo.x; v[z][1] = lo.y; v[z][2] = lo.z; v[z][3] = lo.w;
-          v[z][4] = hi.x; v[z][5] = hi.y; v[z][6] = hi.z; v[z][7] = hi.w;
+          lo = p[0];
+          hi = p[1];
         }
+        v[h][0] = lo.x; v[h][1] = lo.y; v[h][2] = lo.z; v[h][3] = lo.w;
+        v[h][4] = hi.x; v[h][5] = hi.y; v[h][6] = hi.z; v[h][7] = hi.w;
       }
+      put(v, max(amax8(v[0]), amax8(v[1])), kb0 * kBlk, kb0, 0);
     } else {
-      uint4 ug[kUnroll], uu[kUnroll], ud[kUnroll];
+      uint4 ug[2], uu[2], ud[2];
 #pragma unroll
-      for (int z = 0; z < kUnroll; ++z) {
-        const int c = (kb0 + z) * kBlk + hl * 8;
-        ug[z] = uu[z] = ud[z] = make_uint4(0, 0, 0, 0);
-        if (live && kb0 + z < kb1 && c < a.K) {
+      for (int h = 0; h < 2; ++h) {
+        const int c = kb0 * kBlk + 64 * h;
+        ug[h] = uu[h] = ud[h] = make_uint4(0, 0, 0, 0);
+        if (in(c)) {
           const uint16_t* p = static_cast<const uint16_t*>(a.x) + row + c;
-          ug[z] = *(reinterpret_cast<const uint4*>(p));
-          uu[z] = *(reinterpret_cast<const uint4*>(p + a.K));
-          if (KIND == kQuantGluBackward)
-            ud[z] = *(reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(r) * a.ld_dh + c));
+          ug[h] = *reinterpret_cast<const uint4*>(p);
+          uu[h] = *reinterpret_cast<const uint4*>(p + a.K);
+          if (GRAD) ud[h] = *reinterpret_cast<const uint4*>(dh + c);
         }
       }
+      float g[2][8], u[2][8];
 #pragma unroll
-      for (int z = 0; z < kUnroll; ++z) {
-        float g[8], u[8], d[8];
-        unpack8(ug[z], g);
-        unpack8(uu[z], u);
-        unpack8(ud[z], d);
+      for (int h = 0; h < 2; ++h) {
+        float d[8];
+        unpack8(ug[h], g[h]);
+        unpack8(uu[h], u[h]);
+        unpack8(ud[h], d);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float av, bv, da = 0.f, db = 0.f;
-          glu_parts(g[i], u[i], a, KIND == kQuantGluBackward, av, bv, da, db);
-          if constexpr (KIND == kQuantGluBackward) {
-            v[z][i] = d[i] * bv * da;
-            w[z][i] = d[i] * av * db;
+          glu_parts<GLU, GRAD>(g[h][i], u[h][i], a, av, bv, da, db);
+          if (GRAD) {
+            g[h][i] = d[i] * bv * da;
+            u[h][i] = GLU == kSwiglu ? d[i] * av : d[i] * av * db;
           } else {
-            v[z][i] = av * bv;
+            g[h][i] = av * bv;
           }
         }
       }
-    }
-#pragma unroll
-    for (int z = 0; z < kUnroll; ++z) {
-      const int kb = kb0 + z, c = kb * kBlk + hl * 8;
-      const bool in = live && kb < kb1;
-      const int width = KIND == kQuantGluBackward ? 2 * a.K : a.K;
-      uint8_t* out = a.codes + static_cast<size_t>(r) * width + c;
-      const BlockScale b = block_scale(half_warp_max(amax8(v[z])));
-      if (in && c < a.K) *reinterpret_cast<uint2*>(out) = codes8(v[z], b);
-      if (in && hl == 0) a.scales[static_cast<size_t>(kb) * a.ld_s + r] = b.s;
-      if constexpr (KIND == kQuantGluBackward) {
-        // K is a multiple of 128 here: the up half's blocks follow the gate half's.
-        const BlockScale bu = block_scale(half_warp_max(amax8(w[z])));
-        if (in) *reinterpret_cast<uint2*>(out + a.K) = codes8(w[z], bu);
-        if (in && hl == 0) a.scales[static_cast<size_t>(nkb + kb) * a.ld_s + r] = bu.s;
-      }
+      put(g, max(amax8(g[0]), amax8(g[1])), kb0 * kBlk, kb0, 0);
+      // K is a multiple of 128 for the gradient: the up half's blocks follow.
+      if (GRAD) put(u, max(amax8(u[0]), amax8(u[1])), kb0 * kBlk, nkb + kb0, a.K);
     }
   }
 }
@@ -269,11 +373,7 @@ __global__ void __launch_bounds__(256) k_quant_weights_block(const uint16_t* w, 
     if (n < N && c < K) u[i] = *(reinterpret_cast<const uint4*>(w + base + static_cast<size_t>(n) * K + c));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float v[8];
-    unpack8(u[i], v);
-    m = max(m, amax8(v));
-  }
+  for (int i = 0; i < 8; ++i) m = max(m, amax8(u[i]));
   m = __reduce_max_sync(kFull, m);
   if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
   __syncthreads();
@@ -287,23 +387,38 @@ __global__ void __launch_bounds__(256) k_quant_weights_block(const uint16_t* w, 
     if (n >= N || c >= K) continue;
     float v[8];
     unpack8(u[i], v);
-    *reinterpret_cast<uint2*>(codes + base + static_cast<size_t>(n) * K + c) = codes8(v, b);
+    uint2 q = codes8_bf16(v, b);
+    if (b.inv == 0.f) q = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(codes + base + static_cast<size_t>(n) * K + c) = q;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_quant_blocks(const QuantArgs& a, int kind, cudaStream_t s) {
+namespace {
+template <int KIND, int GLU = kSwiglu>
+cudaError_t launch_kind(const QuantArgs& a, cudaStream_t s) {
+  constexpr int U = kUnroll<KIND>;
   const int nkb = (a.K + kBlk - 1) / kBlk;
-  // Every CTA takes kUnroll blocks of its rows at a time; few rows spread their
-  // columns over more CTAs.
-  const int gy = (nkb + kUnroll - 1) / kUnroll;
-  const dim3 grid((a.R + kRowsPerCta - 1) / kRowsPerCta, gy), block(256);
+  const int gx = (a.R + kRowsPerCta - 1) / kRowsPerCta;
+  // A CTA walks its rows' blocks U at a time; few rows spread their columns over
+  // more CTAs, until there are several for every SM.
+  const int gy = std::min((nkb + U - 1) / U, std::max(1, (148 * 8 + gx - 1) / gx));
+  return launch_k(k_quant_blocks<KIND, GLU>, dim3(gx, gy), dim3(256), 0, s, false, a);
+}
+template <int KIND>
+cudaError_t launch_glu(const QuantArgs& a, cudaStream_t s) {
+  if (a.act == MOE_ACT_SITU_GLU) return launch_kind<KIND, kSitu>(a, s);
+  return a.clamped ? launch_kind<KIND, kSwigluClamped>(a, s) : launch_kind<KIND, kSwiglu>(a, s);
+}
+}  // namespace
+
+cudaError_t launch_quant_blocks(const QuantArgs& a, int kind, cudaStream_t s) {
   switch (kind) {
-    case kQuantBf16: return launch_k(k_quant_blocks<kQuantBf16>, grid, block, 0, s, false, a);
-    case kQuantF32: return launch_k(k_quant_blocks<kQuantF32>, grid, block, 0, s, false, a);
-    case kQuantGlu: return launch_k(k_quant_blocks<kQuantGlu>, grid, block, 0, s, false, a);
-    default: return launch_k(k_quant_blocks<kQuantGluBackward>, grid, block, 0, s, false, a);
+    case kQuantBf16: return launch_kind<kQuantBf16>(a, s);
+    case kQuantF32: return launch_kind<kQuantF32>(a, s);
+    case kQuantGlu: return launch_glu<kQuantGlu>(a, s);
+    default: return launch_glu<kQuantGluBackward>(a, s);
   }
 }
 

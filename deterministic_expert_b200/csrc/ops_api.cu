@@ -200,6 +200,7 @@ static int glu_args(const moe_glu_config* cfg, int rows, int I, const moe_bf16* 
   a->scales = scales;
   a->ld_s = ld_s;
   a->act = cfg->activation;
+  a->clamped = std::isfinite(cfg->gate_clamp_max) || std::isfinite(cfg->up_clamp);
   a->gate_clamp = cfg->gate_clamp_max;
   a->up_clamp = cfg->up_clamp;
   a->beta_g = cfg->situ_beta_gate;

@@ -65,6 +65,7 @@ struct QuantArgs {
   float* scales;               // [blocks of 128, ld_s]
   long long ld_s;
   int act;
+  int clamped;                 // a SwiGLU clamp is finite
   float gate_clamp, up_clamp, beta_g, beta_u;
 };
 enum QuantKind : int { kQuantBf16 = 0, kQuantF32 = 1, kQuantGlu = 2, kQuantGluBackward = 3 };
