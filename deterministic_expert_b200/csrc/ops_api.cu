@@ -110,6 +110,7 @@ int moe_route(const moe_route_config* cfg, int T, const void* logits, long long 
   a.idx = out_idx;
   a.w = out_w;
   a.vec = a.cpl * a.lpg == a.gs && (a.cpl * size) % 16 == 0 && al(logits, 16) && pitch16(ld, size);
+  a.vec_bias = a.cpl * a.lpg == a.gs && a.cpl % 4 == 0 && al(bias, 16);
   return status(launch_route(a, cfg->logits_dtype == MOE_DTYPE_BF16, static_cast<cudaStream_t>(stream)));
 }
 

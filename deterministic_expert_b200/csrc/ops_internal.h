@@ -28,6 +28,7 @@ struct RouteOpArgs {
   int lpg;              // lanes per group (a power of two)
   int cpl;              // experts per lane
   int vec;              // rows may be read 16 bytes at a time (cpl * size a multiple of 16)
+  int vec_bias;         // the same for the bias
   int renorm;
   float scale;
   int32_t* idx;         // [T, k]

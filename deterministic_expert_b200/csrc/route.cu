@@ -11,9 +11,10 @@
 //
 // Selection follows the keys' order in exact arithmetic.  Without a bias the
 // scores grow with the logits, so the logits themselves are the keys and every
-// comparison is exact.  With one, keys are formed in fp32 and two neighbours in
-// the order that lie within the error bound below send the row to a second pass
-// in fp64 (about two rows in a thousand of normal logits).
+// comparison is exact.  With one, keys are formed in fp32; where two neighbours in
+// the order lie within the error bound below, the slots' keys (and those of the
+// experts just left out) are formed again in fp64, one a lane; a row whose groups
+// are that close goes to a second pass that is fp64 throughout.
 #include <cfloat>
 
 #include "common.cuh"
@@ -28,8 +29,8 @@ constexpr unsigned kFull = 0xffffffffu;
 // fp32 as an unsigned integer of the same order; 0 is below every number (it
 // stands for "cannot be chosen").  -0 and +0 are one value.
 __device__ __forceinline__ uint32_t order_of(float v) {
-  const uint32_t b = __float_as_uint(v + 0.0f);
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int b = __float_as_int(v + 0.0f);
+  return static_cast<uint32_t>(b ^ ((b >> 31) | 0x80000000));
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
@@ -55,11 +56,35 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// How far two fp32 keys of about this size can be from their exact difference.
-// sigmoid: expf 2 ulp, the sum and the division half an ulp each: below 1.8e-7 for
-// s <= 1; softmax: the argument's rounding and the fp32 sum of up to 1024 terms
-// add about 4e-7 s; the sum with the bias 2^-24 |key|.  Doubled for two keys.
-__device__ __forceinline__ float close_bound(float key) { return 1.2e-6f + 2.5e-7f * fabsf(key); }
+// The same to about 1e-7: its own rounding and the exponent's, |l| s (1 - s) 2^-23 at
+// most (for keys, whose near neighbours are settled in fp64).
+__device__ __forceinline__ float sigmoid_fast(float l) { return __fdividef(1.0f, 1.0f + __expf(-l)); }
+
+// Descending, by Batcher's odd-even merge network.
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+      for (int j = q % p; j <= N - 1 - q; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i <= N - j - q - 1 && (i + j) / (p * 2) == (i + j + q) / (p * 2)) {
+            const uint32_t hi = max(v[i + j], v[i + j + q]), lo = min(v[i + j], v[i + j + q]);
+            v[i + j] = hi;
+            v[i + j + q] = lo;
+          }
+}
+
+// How far the difference of two fp32 keys of about this size can be from the exact
+// one.  sigmoid: below 3e-7 for s <= 1 (sigmoid_fast); softmax: the argument's
+// rounding, expf and the fp32 sum of up to 1024 terms, below 5e-7; the sum with the
+// bias 2^-24 |key|.  Each twice, for two keys.
+__device__ __forceinline__ float close_bound(float key, int softmax) {
+  return fmaf(1.3e-7f, fabsf(key), softmax ? 1.1e-6f : 6.5e-7f);
+}
 
 // The whole row again in fp64, for rows whose fp32 keys are too close to order.
 // Returns the expert of slot `lane` (-1: none).
@@ -151,9 +176,10 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, in
 
 // One warp per token.  Lane l owns cpl consecutive experts of group l / lpg, so
 // lanes hold experts in index order: the lowest lane with the greatest key, and
-// its first position with it, is the lowest index.  Each of the k rounds takes
-// the maximum of the lanes' heads with one redux and refreshes the winner's head;
-// lane j ends with slot j.
+// its first position with it, is the lowest index.  Every lane sorts its keys; each
+// of the k rounds takes the maximum of the lanes' heads with one redux and the
+// winner moves up its list; lane j notes the key and the winner of slot j and looks
+// its expert up among the winner's keys when all are known.
 // Bound by instructions issued: T = 8192, E = 256, k = 8 in 8 groups reads 8.4 MB.
 template <int CPL, typename In>
 __global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
@@ -202,24 +228,41 @@ __global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
   }
   auto score = [&](float v) { return a.softmax ? expf(v - rmax) / rsum : sigmoid_f32(v); };
 
-  uint32_t key[CPL];
+  uint32_t key[CPL], top[CPL];   // in index order; descending
+  const float rscale = 1.f / rsum;
   if (a.bias != nullptr) {
+    float bias[CPL];
+    bool whole = false;
+    if constexpr (CPL >= 4) if (a.vec_bias) {
+      whole = true;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i)
-      key[i] = (i < count && l[i] > -INFINITY) ? key_of(score(l[i]) + a.bias[first + i]) : 0u;
+      for (int i = 0; i < CPL; i += 4) {
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < count) f = *reinterpret_cast<const float4*>(a.bias + first + i);
+        bias[i] = f.x; bias[i + 1] = f.y; bias[i + 2] = f.z; bias[i + 3] = f.w;
+      }
+    }
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) bias[i] = i < count ? a.bias[first + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const float s = a.softmax ? expf(l[i] - rmax) * rscale : sigmoid_fast(l[i]);
+      key[i] = l[i] > -INFINITY ? key_of(s + bias[i]) : 0u;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < CPL; ++i) key[i] = key_of(l[i]);
   }
 
-  bool close = false;   // an order that fp32 cannot decide
-  if (groups) {
-    uint32_t m1 = 0, m2 = 0;
 #pragma unroll
-    for (int i = 0; i < CPL; ++i) {
-      m2 = max(m2, min(m1, key[i]));
-      m1 = max(m1, key[i]);
-    }
+  for (int i = 0; i < CPL; ++i) top[i] = key[i];
+  sort_desc(top);
+
+  bool close_groups = false;   // an order that fp32 cannot decide
+  if (groups) {
+    uint32_t m1 = top[0], m2 = CPL > 1 ? top[1] : 0u;
     for (int o = 1; o < a.lpg; o <<= 1) {
       const uint32_t o1 = __shfl_xor_sync(kFull, m1, o), o2 = __shfl_xor_sync(kFull, m2, o);
       m2 = max(max(m2, o2), min(m1, o1));
@@ -243,44 +286,88 @@ __global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
       const uint32_t best = __reduce_max_sync(kFull, g < a.n_groups && !stays ? gscore : 0u);
       if (best != 0 && worst != 0xffffffffu) {
         const float vw = value_of(worst), vb = value_of(best);
-        close = vw - vb <= 2.f * close_bound(vw);
+        close_groups = vw - vb <= 2.f * close_bound(vw, a.softmax);
       }
     }
     if (!stays) {
 #pragma unroll
-      for (int i = 0; i < CPL; ++i) key[i] = 0;
+      for (int i = 0; i < CPL; ++i) top[i] = 0;
     }
   }
 
-  int chosen = -1;
-  uint32_t head = 0;
-#pragma unroll
-  for (int i = 0; i < CPL; ++i) head = max(head, key[i]);
-  // With fp32 keys one round more than k: the first expert left out.
-  const int rounds = a.bias != nullptr ? a.k + 1 : a.k;
-  uint32_t prev = 0;
-  for (int j = 0; j < rounds; ++j) {
-    const uint32_t m = __reduce_max_sync(kFull, head);
+  // Rounds beyond the k-th only with fp32 keys: the experts left out that come within
+  // the bound of the last one in.
+  bool close = false, many = false;
+  uint32_t prev = 0, mine = 0;   // mine: the key of this lane's slot (0: none)
+  int from = 0;                  // and the lane that had it
+  float last = 0.f;              // key of slot k - 1
+  for (int j = 0;; ++j) {
+    if (a.bias == nullptr && j == a.k) break;
+    const uint32_t m = __reduce_max_sync(kFull, top[0]);
     if (m == 0) break;
-    if (a.bias != nullptr && j > 0) close |= value_of(prev) - value_of(m) <= close_bound(value_of(prev));
-    prev = m;
-    if (j == a.k) break;
-    const int win = __ffs(__ballot_sync(kFull, head == m)) - 1;
-    int e = -1;
-    if (lane == win) {
-      head = 0;
-#pragma unroll
-      for (int i = 0; i < CPL; ++i) {
-        if (e < 0 && key[i] == m) { e = first + i; key[i] = 0; }
-        head = max(head, key[i]);
+    if (a.bias != nullptr) {
+      const float v = value_of(m);
+      if (j > 0) close |= value_of(prev) - v <= close_bound(v, a.softmax);
+      if (j >= a.k) {
+        if (j == a.k) last = value_of(prev);
+        if (!close || last - v > close_bound(v, a.softmax)) break;
+        if (j == 32) { many = true; break; }
       }
+      prev = m;
     }
-    e = __shfl_sync(kFull, e, win);
-    if (lane == j) chosen = e;
+    const int win = __ffs(__ballot_sync(kFull, top[0] == m)) - 1;
+    if (lane == j) { mine = m; from = win; }
+    const bool up = lane == win;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) top[i] = up ? (i + 1 < CPL ? top[i + 1] : 0u) : top[i];
   }
-  if (close) chosen = select_exact<CPL, In>(a, row, lane, first, count);   // uniform over the warp
+  // Slot `lane`: the expert of lane `from` with key `mine`; of several equal ones the
+  // one after those that earlier slots took.
+  int chosen = -1;
+  {
+    // Equal keys of one lane fill neighbouring slots: how many before this one.
+    const uint32_t mine_below = __shfl_up_sync(kFull, mine, 1);   // every lane takes part in both
+    const int from_below = __shfl_up_sync(kFull, from, 1);
+    const bool same = lane > 0 && mine_below == mine && from_below == from;
+    const unsigned starts = ~__ballot_sync(kFull, same) & (0xffffffffu >> (31 - lane));
+    int skip = lane - (31 - __clz(starts));
+    const int f0 = __shfl_sync(kFull, first, from);
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+      const uint32_t v = __shfl_sync(kFull, key[i], from);
+      if (mine != 0 && v == mine && chosen < 0 && skip-- == 0) chosen = f0 + i;
+    }
+  }
+  int slot = lane;
+  if (close_groups || many) {   // uniform over the warp, as close
+    chosen = select_exact<CPL, In>(a, row, lane, first, count);
+  } else if (close) {
+    double m = 0.0, sum = 1.0, k64 = -static_cast<double>(INFINITY);
+    if (a.softmax) {
+      m = rmax;
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+        if (l[i] > -INFINITY) sum += exp(static_cast<double>(l[i]) - m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    }
+    if (chosen >= 0) {
+      const double v = static_cast<double>(to_float(row[chosen]));
+      k64 = (a.softmax ? exp(v - m) / sum : 1.0 / (1.0 + exp(-v))) + static_cast<double>(a.bias[chosen]);
+    }
+    const int n = __popc(__ballot_sync(kFull, chosen >= 0));   // slots 0 .. n - 1 are filled
+    int rank = 0;
+    for (int j = 0; j < n; ++j) {
+      const double kj = __shfl_sync(kFull, k64, j);
+      const int ej = __shfl_sync(kFull, chosen, j);
+      rank += (kj > k64 || (kj == k64 && ej < chosen)) ? 1 : 0;
+    }
+    if (chosen >= 0) slot = rank;
+  }
+  if (slot >= a.k) chosen = -1;
 
-  // Weights: lane j has slot j.
+  // Weights; every lane has one slot.
   const bool have = chosen >= 0;
   const float lj = have ? to_float(row[chosen]) : -INFINITY;
   float w = 0.f;
@@ -301,9 +388,9 @@ __global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
   } else if (have) {
     w = score(lj) * a.scale;
   }
-  if (lane < a.k) {
-    a.idx[static_cast<long long>(t) * a.k + lane] = chosen;
-    a.w[static_cast<long long>(t) * a.k + lane] = w;
+  if (slot < a.k) {
+    a.idx[static_cast<long long>(t) * a.k + slot] = chosen;
+    a.w[static_cast<long long>(t) * a.k + slot] = w;
   }
 }
 
@@ -425,14 +512,27 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
 // ---------------------------------------------------------------- grouping
 // One cluster of 8 CTAs; CTA c takes the c-th eighth of the flattened (token,
 // slot) list and each of its warps a run of it.  A warp walks its run 32 entries
-// at a time (match.any ranks equal experts inside them) counting per expert in
-// its own row of shared memory; the prefix over warps, over CTAs (through
+// at a time, counting per expert in its own row of shared memory (the lanes with
+// one expert come from a vote on each of its bits: match.any costs the SM about 40
+// cycles a time, which doubled the kernel); the prefix over warps, over CTAs (through
 // distributed shared memory) and over experts gives every warp its first row of
 // every expert; a second walk hands the rows out.  Integers only, the order is the
 // list's: stable by token, then slot.  No workspace and one launch, whatever T.
 // Bound by latency: the list is small (T = 8192, k = 8: 262 KB).
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
+constexpr int kAtOnce = 8;
+
+// Lanes whose `e` (its `bits` low bits) equals this lane's.
+__device__ __forceinline__ unsigned lanes_with(int e, int bits) {
+  unsigned same = kFull;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = (e >> b) & 1;
+    const unsigned v = __ballot_sync(kFull, one);
+    same &= one ? v : ~v;
+  }
+  return same;
+}
 
 __global__ void __launch_bounds__(kGroupThreads)
     k_group_rows(const int32_t* idx, int n, int k, int E, int32_t* offsets,
@@ -444,23 +544,37 @@ __global__ void __launch_bounds__(kGroupThreads)
   __shared__ int32_t warp_tot[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int cta = static_cast<int>(cluster_ctarank());
-  // Runs are whole multiples of 32 entries.
-  const long long per_warp = ((static_cast<long long>(n) + kGroupCtas * kWarps - 1) / (kGroupCtas * kWarps) + 31) / 32 * 32;
-  const long long lo = min(static_cast<long long>(n), (static_cast<long long>(cta) * kWarps + warp) * per_warp);
-  const long long hi = min(static_cast<long long>(n), lo + per_warp);
+  // Runs are whole multiples of 32 entries; n < 2^31.
+  const uint32_t per_warp = ((static_cast<uint32_t>(n) + kGroupCtas * kWarps - 1) / (kGroupCtas * kWarps) + 31) / 32 * 32;
+  const uint32_t lo = static_cast<uint32_t>(min(static_cast<unsigned long long>(n),
+                                                (static_cast<unsigned long long>(cta) * kWarps + warp) * per_warp));
+  const uint32_t hi = static_cast<uint32_t>(min(static_cast<unsigned long long>(n),
+                                                static_cast<unsigned long long>(lo) + per_warp));
   for (int i = tid; i < kWarps * E; i += kGroupThreads) hist[i] = 0;
   griddep_wait();
   griddep_launch();
   __syncthreads();
 
   int32_t* h = hist + warp * E;
-  for (long long b = lo; b < hi; b += 32) {
-    const long long i = b + lane;
-    const int e = i < hi ? idx[i] : -1;
-    const bool ok = e >= 0 && e < E;
-    const unsigned same = __match_any_sync(kFull, ok ? e : -1);
-    if (ok && lane == __ffs(same) - 1) h[e] += __popc(same);
-    __syncwarp();
+  const int bits = 32 - __clz(E);   // E itself stands for no expert
+  // kAtOnce loads are in flight before their entries are counted.
+  int e[kAtOnce];
+  auto read = [&](uint32_t b) {
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z) {
+      const uint32_t i = b + 32 * z + lane;
+      e[z] = i < hi ? idx[i] : -1;
+      if (e[z] >= E) e[z] = -1;
+    }
+  };
+  for (uint32_t b = lo; b < hi; b += 32 * kAtOnce) {
+    read(b);
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z) {
+      const unsigned same = lanes_with(e[z] < 0 ? E : e[z], bits);
+      if (e[z] >= 0 && lane == __ffs(same) - 1) h[e[z]] += __popc(same);
+      __syncwarp();
+    }
   }
   __syncthreads();
   for (int e = tid; e < E; e += kGroupThreads) {
@@ -510,19 +624,22 @@ __global__ void __launch_bounds__(kGroupThreads)
     for (int w = 0; w < kWarps; ++w) hist[w * E + tid] += add;
   }
   __syncthreads();
-  for (long long b = lo; b < hi; b += 32) {
-    const long long i = b + lane;
-    const int e = i < hi ? idx[i] : -1;
-    const bool ok = e >= 0 && e < E;
-    const unsigned same = __match_any_sync(kFull, ok ? e : -1);
-    int pos = -1;
-    if (ok) pos = h[e] + __popc(same & ((1u << lane) - 1u));
-    __syncwarp();
-    if (ok && lane == __ffs(same) - 1) h[e] += __popc(same);
-    __syncwarp();
-    if (i < hi) {
-      row_of_slot[i] = pos;
-      if (ok) token_of_row[pos] = static_cast<int32_t>(i / k);
+  for (uint32_t b = lo; b < hi; b += 32 * kAtOnce) {
+    if (hi - lo > 32 * kAtOnce) read(b);   // else still there from the count
+#pragma unroll
+    for (int z = 0; z < kAtOnce; ++z) {
+      const uint32_t i = b + 32 * z + lane;
+      const bool ok = e[z] >= 0;
+      const unsigned same = lanes_with(ok ? e[z] : E, bits);
+      int pos = -1;
+      if (ok) pos = h[e[z]] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (ok && lane == __ffs(same) - 1) h[e[z]] += __popc(same);
+      __syncwarp();
+      if (i < hi) {
+        row_of_slot[i] = pos;
+        if (ok) token_of_row[pos] = static_cast<int32_t>(i / static_cast<uint32_t>(k));
+      }
     }
   }
   // Rows behind the last group come from no token.
