@@ -511,22 +511,24 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
 
 // ---------------------------------------------------------------- grouping
 // One cluster of 8 CTAs; CTA c takes the c-th eighth of the flattened (token,
-// slot) list and each of its warps a run of it.  A warp walks its run 32 entries
-// at a time, counting per expert in its own row of shared memory (the lanes with
-// one expert come from a vote on each of its bits: match.any costs the SM about 40
-// cycles a time, which doubled the kernel); the prefix over warps, over CTAs (through
+// slot) list and each of its warps a run of it.  A warp counts its run per expert
+// in its own row of shared memory; the prefix over warps, over CTAs (through
 // distributed shared memory) and over experts gives every warp its first row of
-// every expert; a second walk hands the rows out.  Integers only, the order is the
+// every expert; a second walk hands the rows out 32 entries at a time (the lanes
+// with one expert come from a vote on each of its bits: match.any costs the SM
+// about 40 cycles a time).  Integers only, the order is the
 // list's: stable by token, then slot.  No workspace and one launch, whatever T.
 // Bound by latency: the list is small (T = 8192, k = 8: 262 KB).
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
 constexpr int kAtOnce = 8;
 
-// Lanes whose `e` (its `bits` low bits) equals this lane's.
+// Lanes whose `e` (its `bits` low bits, at most 11) equals this lane's.
 __device__ __forceinline__ unsigned lanes_with(int e, int bits) {
   unsigned same = kFull;
-  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+  for (int b = 0; b < 11; ++b) {
+    if (b >= bits) break;   // uniform
     const bool one = (e >> b) & 1;
     const unsigned v = __ballot_sync(kFull, one);
     same &= one ? v : ~v;
@@ -571,9 +573,7 @@ __global__ void __launch_bounds__(kGroupThreads)
     read(b);
 #pragma unroll
     for (int z = 0; z < kAtOnce; ++z) {
-      const unsigned same = lanes_with(e[z] < 0 ? E : e[z], bits);
-      if (e[z] >= 0 && lane == __ffs(same) - 1) h[e[z]] += __popc(same);
-      __syncwarp();
+      if (e[z] >= 0) atomicAdd(&h[e[z]], 1);   // a count: any order
     }
   }
   __syncthreads();

@@ -10,8 +10,8 @@ current one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -49,6 +49,9 @@ ARGTYPES = {
     "moe_get_operator_error": [_vp],
 }
 _fns: dict = {}
+_Tensor = torch.Tensor
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _fn(name):
@@ -62,27 +65,27 @@ def _fn(name):
 
 def _call(name, device, stream, *args):
     """Run an entry point with the tensors' device current, on `stream`."""
-    f = _fn(name)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            rc = f(*args, _on(stream, device))
+    f = _fns.get(name) or _fn(name)
+    s = _raw_stream(device.index) if stream is None else _handle(stream)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, s)
     else:
-        rc = f(*args, _on(stream, device))
+        with torch.cuda.device(device):
+            rc = f(*args, s)
     if rc != 0:
         raise _moe.MoEError(rc, name)
 
 
-def _on(stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+def _handle(stream):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _alloc(stream, device):
-    """Outputs belong to the stream that writes them."""
+def _empty(stream, device, *specs):
+    """New tensors (shape, dtype); they belong to the stream that writes them."""
     if stream is None:
-        return contextlib.nullcontext()
-    return torch.cuda.stream(_moe._torch_stream(stream, device))
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    with torch.cuda.stream(_moe._torch_stream(stream, device)):
+        return [torch.empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
 
 
 def _need(cond, what):
@@ -92,35 +95,42 @@ def _need(cond, what):
 
 def _tensor(t, name, device, dtypes, shape=None, contiguous=True):
     """Refuse a tensor the library would read or write wrongly."""
-    _need(isinstance(t, torch.Tensor), f"{name}: expected a tensor")
+    if (isinstance(t, _Tensor) and t.is_cuda and (device is None or t.device == device) and t.dtype in dtypes
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+        return
+    _need(isinstance(t, _Tensor), f"{name}: expected a tensor")
     _need(t.is_cuda and (device is None or t.device == device),
           f"{name}: expected a CUDA tensor" + (f" on {device}, got {t.device}" if device is not None else ""))
     _need(t.dtype in dtypes, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if shape is not None:
-        _need(tuple(t.shape) == tuple(shape), f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous:
-        _need(t.is_contiguous(), f"{name}: expected a contiguous tensor")
+    _need(shape is None or t.shape == shape, f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
 def _rows(t, name):
     """Row pitch of a matrix whose rows are dense."""
+    if t.dim() == 2:
+        rows, width = t.shape
+        pitch, step = t.stride()
+        if width <= 1 or step == 1:
+            if rows <= 1:
+                return max(width, 1)
+            if pitch >= width:
+                return pitch
     _need(t.dim() == 2, f"{name}: expected two dimensions, got {t.dim()}")
     _need(t.shape[1] <= 1 or t.stride(1) == 1, f"{name}: expected rows of neighbouring elements")
-    if t.shape[0] <= 1:
-        return max(int(t.shape[1]), 1)
-    _need(t.stride(0) >= t.shape[1], f"{name}: rows overlap")
-    return int(t.stride(0))
+    raise ValueError(f"{name}: rows overlap")
 
 
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 _I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
 
 
-def _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale):
+@functools.lru_cache(maxsize=256)
+def _route_config(E, k, dtype, scores, n_groups, topk_groups, group_top, renormalize, routed_scale):
     _need(scores in ("softmax", "sigmoid"), f"scores: expected 'softmax' or 'sigmoid', got {scores!r}")
     return moe_route_config(E, int(k), _moe.ROUTER_SOFTMAX if scores == "softmax" else _moe.ROUTER_SIGMOID_BIAS,
                             int(n_groups), int(topk_groups), int(group_top), 1 if renormalize else 0,
-                            float(routed_scale), _DTYPES[logits.dtype])
+                            float(routed_scale), _DTYPES[dtype])
 
 
 def route(logits, k: int, *, scores: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
@@ -134,14 +144,16 @@ def route(logits, k: int, *, scores: str = "softmax", bias=None, n_groups: int =
     T, E = int(logits.shape[0]), int(logits.shape[1])
     if bias is not None:
         _tensor(bias, "bias", dev, _F32, (E,))
-    cfg = _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
+    cfg = _route_config(E, k, logits.dtype, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
     _need(cfg.k >= 0, "k: negative")
-    if out_idx is None or out_w is None:
-        with _alloc(stream, dev):
-            out_idx = torch.empty((T, cfg.k), dtype=torch.int32, device=dev) if out_idx is None else out_idx
-            out_w = torch.empty((T, cfg.k), dtype=torch.float32, device=dev) if out_w is None else out_w
-    _tensor(out_idx, "out_idx", dev, _I32, (T, cfg.k))
-    _tensor(out_w, "out_w", dev, _F32, (T, cfg.k))
+    if out_idx is None:
+        out_idx, = _empty(stream, dev, ((T, cfg.k), torch.int32))
+    else:
+        _tensor(out_idx, "out_idx", dev, _I32, (T, cfg.k))
+    if out_w is None:
+        out_w, = _empty(stream, dev, ((T, cfg.k), torch.float32))
+    else:
+        _tensor(out_w, "out_w", dev, _F32, (T, cfg.k))
     _call("moe_route", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld,
           None if bias is None else bias.data_ptr(), out_idx.data_ptr(), out_w.data_ptr())
     return out_idx, out_w
@@ -159,10 +171,9 @@ def route_backward(logits, idx, dw, *, scores: str = "softmax", n_groups: int = 
     k = int(idx.shape[1])
     _tensor(idx, "idx", dev, _I32, (T, k))
     _tensor(dw, "dw", dev, _F32, (T, k))
-    cfg = _route_config(E, k, logits, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
+    cfg = _route_config(E, k, logits.dtype, scores, n_groups, topk_groups, group_top, renormalize, routed_scale)
     if out is None:
-        with _alloc(stream, dev):
-            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        out, = _empty(stream, dev, ((T, E), logits.dtype))
     _tensor(out, "out", dev, (logits.dtype,), (T, E), contiguous=False)
     _call("moe_route_backward", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld, idx.data_ptr(),
           dw.data_ptr(), out.data_ptr(), _rows(out, "out"))
@@ -177,14 +188,13 @@ def group_rows(idx, E: int, *, out=None, stream=None):
     dev = idx.device
     T, k = int(idx.shape[0]), int(idx.shape[1])
     if out is None:
-        with _alloc(stream, dev):
-            out = (torch.empty(max(int(E), 0) + 1, dtype=torch.int32, device=dev),
-                   torch.empty(T * k, dtype=torch.int32, device=dev),
-                   torch.empty((T, k), dtype=torch.int32, device=dev))
-    offsets, token_of_row, row_of_slot = out
-    _tensor(offsets, "offsets", dev, _I32, (int(E) + 1,))
-    _tensor(token_of_row, "token_of_row", dev, _I32, (T * k,))
-    _tensor(row_of_slot, "row_of_slot", dev, _I32, (T, k))
+        offsets, token_of_row, row_of_slot = _empty(stream, dev, ((max(int(E), 0) + 1,), torch.int32),
+                                                    ((T * k,), torch.int32), ((T, k), torch.int32))
+    else:
+        offsets, token_of_row, row_of_slot = out
+        _tensor(offsets, "offsets", dev, _I32, (int(E) + 1,))
+        _tensor(token_of_row, "token_of_row", dev, _I32, (T * k,))
+        _tensor(row_of_slot, "row_of_slot", dev, _I32, (T, k))
     _call("moe_group_rows", dev, stream, T, k, int(E), idx.data_ptr(), offsets.data_ptr(), token_of_row.data_ptr(),
           row_of_slot.data_ptr())
     return offsets, token_of_row, row_of_slot
@@ -192,12 +202,14 @@ def group_rows(idx, E: int, *, out=None, stream=None):
 
 def _quant_out(R, K, out_codes, out_scales, dev, stream):
     nb = -(-K // BLOCK)
-    if out_codes is None or out_scales is None:
-        with _alloc(stream, dev):
-            out_codes = torch.empty((R, K), dtype=torch.uint8, device=dev) if out_codes is None else out_codes
-            out_scales = torch.empty((nb, R), dtype=torch.float32, device=dev) if out_scales is None else out_scales
-    _tensor(out_codes, "out_codes", dev, _CODES, (R, K))
-    _tensor(out_scales, "out_scales", dev, _F32, (nb, R), contiguous=False)
+    if out_codes is None:
+        out_codes, = _empty(stream, dev, ((R, K), torch.uint8))
+    else:
+        _tensor(out_codes, "out_codes", dev, _CODES, (R, K))
+    if out_scales is None:
+        out_scales, = _empty(stream, dev, ((nb, R), torch.float32))
+    else:
+        _tensor(out_scales, "out_scales", dev, _F32, (nb, R), contiguous=False)
     return out_codes, out_scales, _rows(out_scales, "out_scales")
 
 
@@ -238,16 +250,17 @@ def quantize_weights_fp8(w, *, out_codes=None, out_scales=None, stream=None):
     N, K = int(w.shape[-2]), int(w.shape[-1])
     G = int(w.shape[0]) if w.dim() == 3 else 1
     sshape = tuple(w.shape[:-2]) + (-(-N // BLOCK), -(-K // BLOCK))
-    if out_codes is None or out_scales is None:
-        with _alloc(stream, dev):
-            out_codes = torch.empty(w.shape, dtype=torch.uint8, device=dev) if out_codes is None else out_codes
-            out_scales = torch.empty(sshape, dtype=torch.float32, device=dev) if out_scales is None else out_scales
+    if out_codes is None:
+        out_codes, = _empty(stream, dev, (w.shape, torch.uint8))
+    if out_scales is None:
+        out_scales, = _empty(stream, dev, (sshape, torch.float32))
     _tensor(out_codes, "out_codes", dev, _CODES, w.shape)
     _tensor(out_scales, "out_scales", dev, _F32, sshape)
     _call("moe_quantize_weights_fp8", dev, stream, G, N, K, w.data_ptr(), out_codes.data_ptr(), out_scales.data_ptr())
     return out_codes, out_scales
 
 
+@functools.lru_cache(maxsize=256)
 def _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up):
     return moe_glu_config(int(activation), float(gate_clamp_max), float(up_clamp), float(situ_beta_gate),
                           float(situ_beta_up))
@@ -314,8 +327,7 @@ def matmul_fp8(a, a_scale, w, w_scale, *, offsets=None, transposed: bool = False
         _need(G == 1, "offsets: needed with more than one group")
     if out is None:
         _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
-        with _alloc(stream, dev):
-            out = torch.empty((M, width), dtype=out_dtype, device=dev)
+        out, = _empty(stream, dev, ((M, width), out_dtype))
     _tensor(out, "out", dev, tuple(_DTYPES), (M, width), contiguous=False)
     _call("moe_matmul_fp8", dev, stream, 1 if transposed else 0, G, None if offsets is None else offsets.data_ptr(),
           M, N, K, a.data_ptr(), a_scale.data_ptr(), max(ld_as, M), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
@@ -344,8 +356,7 @@ def combine_rows(y, row_of_slot, w=None, *, addend=None, out=None, out_dtype=tor
         _tensor(addend, "addend", dev, _BF16, (T, D))
     if out is None:
         _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
-        with _alloc(stream, dev):
-            out = torch.empty((T, D), dtype=out_dtype, device=dev)
+        out, = _empty(stream, dev, ((T, D), out_dtype))
     _tensor(out, "out", dev, tuple(_DTYPES), (T, D))
     _call("moe_combine_rows", dev, stream, T, k, D, rows, y.data_ptr(), _DTYPES[y.dtype], max(ld, D),
           row_of_slot.data_ptr(), None if w is None else w.data_ptr(),
@@ -364,12 +375,13 @@ def combine_rows_backward(dout, y, row_of_slot, w=None, *, need_dw: bool = True,
     rows, D = int(y.shape[0]), int(y.shape[1])
     T, k = _slots(row_of_slot, w, dev)
     _tensor(dout, "dout", dev, _BF16, (T, D))
-    with _alloc(stream, dev):
-        if out_dy is None:
-            # The pitch of y, as the entry point has one for both.
-            out_dy = torch.empty((rows, ld), dtype=y.dtype, device=dev)[:, :D]
-        if need_dw and out_dw is None:
-            out_dw = torch.empty((T, k), dtype=torch.float32, device=dev)
+    if out_dy is None:
+        # The pitch of y, as the entry point has one for both.
+        out_dy, = _empty(stream, dev, ((rows, ld), y.dtype))
+        if ld != D:
+            out_dy = out_dy[:, :D]
+    if need_dw and out_dw is None:
+        out_dw, = _empty(stream, dev, ((T, k), torch.float32))
     _tensor(out_dy, "out_dy", dev, (y.dtype,), (rows, D), contiguous=False)
     _need(rows <= 1 or _rows(out_dy, "out_dy") == ld, "out_dy: expected the row pitch of y")
     if need_dw:
@@ -385,4 +397,4 @@ def operator_error(device=None, stream=None) -> int:
     the error word of matmul_fp8.  Synchronises the stream."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
-        return int(_fn("moe_get_operator_error")(_on(stream, dev)))
+        return int(_fn("moe_get_operator_error")(_raw_stream(dev.index) if stream is None else _handle(stream)))
