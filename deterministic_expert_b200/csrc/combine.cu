@@ -46,116 +46,139 @@ struct Eight<float> {
   }
 };
 
-// One thread per 8 columns of a token; its slots' loads are issued four at a time
-// before they are added, in slot order.
+// One CTA per token.  Its slots' rows and weights are read once into shared memory;
+// a thread then takes 8 columns at a time, kSlotsAtOnce slots' loads issued before
+// they are added, in slot order.
 // Bound by memory: k rows read, one written.
-constexpr int kSlotsAtOnce = 4;
+constexpr int kSlotsAtOnce = 8;
+
+// Threads for D columns, 8 a thread: as few passes as 256 threads need, evenly.
+int row_threads(int D) {
+  const int chunks = D / 8, passes = (chunks + 255) / 256;
+  return ((chunks + passes - 1) / passes + 31) / 32 * 32;
+}
 
 template <typename Y, typename O>
 __global__ void __launch_bounds__(256) k_combine_rows(const CombineArgs a) {
+  __shared__ int s_row[kRouteMaxK];
+  __shared__ float s_w[kRouteMaxK];
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x;
-  const int c = (blockIdx.y * 256 + threadIdx.x) * 8;
-  if (c >= a.D) return;
-  const Y* y = static_cast<const Y*>(a.y) + c;
-  const int32_t* rows = a.row_of_slot + static_cast<size_t>(t) * a.k;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (a.addend != nullptr) {
-    Eight<uint16_t> e;
-    e.load(a.addend + static_cast<size_t>(t) * a.D + c);
-    e.get(acc);
+  if (threadIdx.x < kRouteMaxK) {
+    int r = -1;
+    float w = 1.f;
+    if (threadIdx.x < a.k) {
+      const size_t i = static_cast<size_t>(t) * a.k + threadIdx.x;
+      r = a.row_of_slot[i];
+      if (a.w != nullptr) w = a.w[i];
+    }
+    s_row[threadIdx.x] = r < a.rows ? r : -1;
+    s_w[threadIdx.x] = w;
   }
-  for (int j0 = 0; j0 < a.k; j0 += kSlotsAtOnce) {
-    Eight<Y> e[kSlotsAtOnce];
-    float w[kSlotsAtOnce];
-    bool ok[kSlotsAtOnce];
+  __syncthreads();
+  for (int c = threadIdx.x * 8; c < a.D; c += blockDim.x * 8) {
+    const Y* y = static_cast<const Y*>(a.y) + c;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.addend != nullptr) {
+      Eight<uint16_t> e;
+      e.load(a.addend + static_cast<size_t>(t) * a.D + c);
+      e.get(acc);
+    }
+    for (int j0 = 0; j0 < a.k; j0 += kSlotsAtOnce) {
+      Eight<Y> e[kSlotsAtOnce];
 #pragma unroll
-    for (int z = 0; z < kSlotsAtOnce; ++z) {
-      const int j = j0 + z;
-      const int r = j < a.k ? rows[j] : -1;
-      ok[z] = r >= 0 && r < a.rows;
-      w[z] = 1.f;
-      if (ok[z]) {
-        e[z].load(y + static_cast<size_t>(r) * a.ld_y);
-        if (a.w != nullptr) w[z] = a.w[static_cast<size_t>(t) * a.k + j];
+      for (int z = 0; z < kSlotsAtOnce; ++z) {
+        const int r = s_row[j0 + z];
+        if (r >= 0) e[z].load(y + static_cast<size_t>(r) * a.ld_y);
+      }
+#pragma unroll
+      for (int z = 0; z < kSlotsAtOnce; ++z) {
+        if (s_row[j0 + z] < 0) continue;
+        const float w = s_w[j0 + z];
+        float v[8];
+        e[z].get(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[i] = fmaf(w, v[i], acc[i]);
       }
     }
-#pragma unroll
-    for (int z = 0; z < kSlotsAtOnce; ++z) {
-      if (!ok[z]) continue;
-      float v[8];
-      e[z].get(v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] = fmaf(w[z], v[i], acc[i]);
-    }
+    Eight<O>::store(static_cast<O*>(a.out) + static_cast<size_t>(t) * a.D + c, acc);
   }
-  Eight<O>::store(static_cast<O*>(a.out) + static_cast<size_t>(t) * a.D + c, acc);
 }
 
-// One CTA per token: a thread keeps its columns of dout, slot by slot reads y,
-// writes dy and adds to the slot's dot product; the products are summed over the
-// CTA in a fixed tree.
+// One CTA per token: a thread takes 8 columns of dout at a time, reads its slots'
+// y, writes their dy and adds to their dot products; the products are summed over
+// the CTA in a fixed tree.
 // Bound by memory: k rows read, k rows written.
+constexpr int kSlotsBack = 2;
+
 template <typename Y>
 __global__ void __launch_bounds__(256) k_combine_rows_backward(const CombineArgs a) {
+  __shared__ float part[kRouteMaxK][8];
+  __shared__ int s_row[kRouteMaxK];
+  __shared__ float s_w[kRouteMaxK];
   griddep_wait();
   griddep_launch();
-  __shared__ float part[kRouteMaxK][8];
   const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int32_t* rows = a.row_of_slot + static_cast<size_t>(t) * a.k;
-  const uint16_t* d = a.dout + static_cast<size_t>(t) * a.D;
-  for (int j0 = 0; j0 < a.k; j0 += kSlotsAtOnce) {
-    float dot[kSlotsAtOnce], w[kSlotsAtOnce];
-    int row[kSlotsAtOnce];
-#pragma unroll
-    for (int z = 0; z < kSlotsAtOnce; ++z) {
-      const int j = j0 + z;
-      row[z] = j < a.k ? rows[j] : -1;
-      if (row[z] >= a.rows) row[z] = -1;
-      w[z] = (row[z] >= 0 && a.w != nullptr) ? a.w[static_cast<size_t>(t) * a.k + j] : 1.f;
-      dot[z] = 0.f;
+  if (threadIdx.x < kRouteMaxK) {
+    int r = -1;
+    float w = 1.f;
+    if (threadIdx.x < a.k) {
+      const size_t i = static_cast<size_t>(t) * a.k + threadIdx.x;
+      r = a.row_of_slot[i];
+      if (a.w != nullptr) w = a.w[i];
     }
-    for (int c = threadIdx.x * 8; c < a.D; c += 256 * 8) {
+    s_row[threadIdx.x] = r < a.rows ? r : -1;
+    s_w[threadIdx.x] = w;
+  }
+  __syncthreads();
+  const uint16_t* d = a.dout + static_cast<size_t>(t) * a.D;
+  for (int j0 = 0; j0 < a.k; j0 += kSlotsBack) {
+    float dot[kSlotsBack] = {};
+    for (int c = threadIdx.x * 8; c < a.D; c += blockDim.x * 8) {
       Eight<uint16_t> ed;
-      Eight<Y> ey[kSlotsAtOnce];
+      Eight<Y> ey[kSlotsBack];
       ed.load(d + c);
       if (a.dw != nullptr) {
 #pragma unroll
-        for (int z = 0; z < kSlotsAtOnce; ++z)
-          if (row[z] >= 0) ey[z].load(static_cast<const Y*>(a.y) + static_cast<size_t>(row[z]) * a.ld_y + c);
+        for (int z = 0; z < kSlotsBack; ++z) {
+          const int r = s_row[j0 + z];
+          if (r >= 0) ey[z].load(static_cast<const Y*>(a.y) + static_cast<size_t>(r) * a.ld_y + c);
+        }
       }
       float dv[8];
       ed.get(dv);
 #pragma unroll
-      for (int z = 0; z < kSlotsAtOnce; ++z) {
-        if (row[z] < 0) continue;
+      for (int z = 0; z < kSlotsBack; ++z) {
+        const int r = s_row[j0 + z];
+        if (r < 0) continue;
+        const float w = s_w[j0 + z];
         float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = dv[i] * w;
+        Eight<Y>::store(static_cast<Y*>(a.dy) + static_cast<size_t>(r) * a.ld_y + c, v);
         if (a.dw != nullptr) {
           ey[z].get(v);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dot[z] = fmaf(dv[i], v[i], dot[z]);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = dv[i] * w[z];
-        Eight<Y>::store(static_cast<Y*>(a.dy) + static_cast<size_t>(row[z]) * a.ld_y + c, v);
       }
     }
     if (a.dw != nullptr) {
 #pragma unroll
-      for (int z = 0; z < kSlotsAtOnce; ++z) {
+      for (int z = 0; z < kSlotsBack; ++z) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot[z] += __shfl_xor_sync(0xffffffffu, dot[z], o);
-        if (lane == 0 && j0 + z < a.k) part[j0 + z][warp] = dot[z];
+        if (lane == 0) part[j0 + z][warp] = dot[z];
       }
     }
   }
   if (a.dw == nullptr) return;
   __syncthreads();
   if (threadIdx.x < a.k) {
+    const int warps = blockDim.x >> 5;
     float s = part[threadIdx.x][0];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) s += part[threadIdx.x][w];
+    for (int w = 1; w < warps; ++w) s += part[threadIdx.x][w];
     a.dw[static_cast<size_t>(t) * a.k + threadIdx.x] = s;
   }
 }
@@ -163,7 +186,7 @@ __global__ void __launch_bounds__(256) k_combine_rows_backward(const CombineArgs
 }  // namespace
 
 cudaError_t launch_combine_rows(const CombineArgs& a, bool y_f32, bool out_f32, cudaStream_t s) {
-  const dim3 grid(a.T, (a.D / 8 + 255) / 256), block(256);
+  const dim3 grid(a.T), block(row_threads(a.D));
   if (y_f32)
     return out_f32 ? launch_k(k_combine_rows<float, float>, grid, block, 0, s, false, a)
                    : launch_k(k_combine_rows<float, uint16_t>, grid, block, 0, s, false, a);
@@ -172,8 +195,9 @@ cudaError_t launch_combine_rows(const CombineArgs& a, bool y_f32, bool out_f32, 
 }
 
 cudaError_t launch_combine_rows_backward(const CombineArgs& a, bool y_f32, cudaStream_t s) {
-  return y_f32 ? launch_k(k_combine_rows_backward<float>, dim3(a.T), dim3(256), 0, s, false, a)
-               : launch_k(k_combine_rows_backward<uint16_t>, dim3(a.T), dim3(256), 0, s, false, a);
+  const dim3 grid(a.T), block(row_threads(a.D));
+  return y_f32 ? launch_k(k_combine_rows_backward<float>, grid, block, 0, s, false, a)
+               : launch_k(k_combine_rows_backward<uint16_t>, grid, block, 0, s, false, a);
 }
 
 }  // namespace moe
