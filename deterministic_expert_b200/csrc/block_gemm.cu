@@ -80,6 +80,29 @@ __device__ __forceinline__ void group_range(const BlockGemmArgs& a, int g, int& 
   hi = min(max(a.offsets[g + 1], lo), a.M);
 }
 
+// First tile of every group (ntn tiles a row of tiles); one warp.
+__device__ __forceinline__ void scan_groups(const BlockGemmArgs& a, int* start, int ntn, int lane) {
+  int run = 0;
+  for (int b = 0; b < a.G; b += 32) {
+    int n = 0;
+    if (b + lane < a.G) {
+      int lo, hi;
+      group_range(a, b + lane, lo, hi);
+      n = (hi - lo + a.tile_rows - 1) / a.tile_rows * ntn;
+    }
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (b + lane < a.G) start[b + lane] = run + incl - n;
+    run += __shfl_sync(kFull, incl, 31);
+  }
+  if (lane == 0) start[a.G] = run;
+}
+
+template <int COLS = 256>
 __device__ __forceinline__ BTile decode(const BlockGemmArgs& a, const int* start, int ntn, int t) {
   int lo = 0, hi = a.G;   // largest g with start[g] <= t
   while (hi - lo > 1) {
@@ -92,7 +115,7 @@ __device__ __forceinline__ BTile decode(const BlockGemmArgs& a, const int* start
   group_range(a, lo, r0, r1);
   const int local = t - start[lo];
   const int m = local / ntn;
-  ti.n0 = (local - m * ntn) * 256;
+  ti.n0 = (local - m * ntn) * COLS;
   ti.row0 = r0 + m * a.tile_rows;
   ti.rows = min(a.tile_rows, r1 - ti.row0);
   ti.swap = ti.rows <= kSwapRows;
@@ -169,8 +192,15 @@ template <int CH>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[CH]) {
   if constexpr (CH == 32) {
     tmem_ld32(taddr, r);
+  } else if constexpr (CH == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
   } else {
-    static_assert(CH == 8, "8 or 32 columns");
+    static_assert(CH == 8, "8, 16 or 32 columns");
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
@@ -180,6 +210,12 @@ template <int CH>
 __device__ __forceinline__ void tmem_wait(uint32_t (&v)[CH]) {
   if constexpr (CH == 32) {
     tmem_wait32(v);
+  } else if constexpr (CH == 16) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
   } else {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
@@ -318,27 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
 
   const int ntn = (a.width + 255) / 256;
   const int nkb = (a.con + 127) / 128;
-  // First tile of every group.
-  if (warp == 2) {
-    int run = 0;
-    for (int b = 0; b < a.G; b += 32) {
-      int n = 0;
-      if (b + lane < a.G) {
-        int lo, hi;
-        group_range(a, b + lane, lo, hi);
-        n = (hi - lo + a.tile_rows - 1) / a.tile_rows * ntn;
-      }
-      int incl = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      if (b + lane < a.G) s_start[b + lane] = run + incl - n;
-      run += __shfl_sync(kFull, incl, 31);
-    }
-    if (lane == 0) s_start[a.G] = run;
-  }
+  if (warp == 2) scan_groups(a, s_start, ntn, lane);
   __syncthreads();
   const int total = s_start[a.G];
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -706,10 +722,256 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
   }
 }
 
+// ------------------------------------------------------------ few tiles
+// Products with too few tiles to fill the device with the kernel above (single
+// tokens against one weight matrix): a cluster of C CTAs takes one tile of 128
+// weight rows x up to 32 rows of A and divides the contraction's blocks into C runs.
+// Each CTA streams its run and keeps its block sums P_b in TMEM, side by side; then
+// the sums walk through the cluster: CTA 0 adds its blocks to zero, hands its
+// 128 x rows fp32 sums to CTA 1 through distributed shared memory, which adds its
+// own, and so on; the last one stores.  Every element is acc = fma(P_b, fl(sa sw),
+// acc) with b ascending, as above: the same bits.
+// Bound by the weights' stream and the walk: a CTA alone streams about 100 GB/s, so
+// the split brings M = 8, N = 4096, K = 7168 from 32 busy SMs to 128 (20 -> 13.3 us);
+// the walk costs about 1.5 us a CTA.
+// Roles: warp 0 TMA, warp 1 MMA, warps 2-3 scales, warps 4-7 sums (a thread one
+// weight row).
+constexpr int kThinThreads = 256;
+constexpr int kThinRing = 176 * 1024;
+constexpr int kThinMost = 12;
+constexpr int kThinRows = 32;
+constexpr int kThinSums = kThinRows * 128 * 4;   // sum_at
+constexpr int kThinSmem = 1024 + kThinRing + 512 + kThinSums + 512 * 4;
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// bar_wait for a barrier that another CTA of the cluster arrives on after writing
+// this CTA's shared memory.
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t abort) {
+  for (int i = 0; i < kTries; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (ld_shared_i32(abort) != 0) return false;
+  }
+  asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(abort) : "memory");
+  atomicExch(&g_operator_error, kDevTimeout);
+  return false;
+}
+
+// Byte of the sums of weight row `row` and rows 4 i .. 4 i + 3 of A: four numbers
+// together, so that a warp moves them 16 bytes a thread without bank conflicts.
+__device__ __forceinline__ uint32_t sum_at(int row, int i) { return (i * 128 + row) * 16; }
+
+template <int TRANS, typename Out>
+__global__ void __launch_bounds__(kThinThreads, 1) k_block_gemm_thin(const __grid_constant__ BlockGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const int S = min(kThinMost, kThinRing / (kWSlot + a.a_slot));
+  uint8_t* sW = smem;
+  uint8_t* sA = smem + S * kWSlot;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ int s_start[kMatmulMaxGroups + 1];
+  const uint32_t smem0 = smem_u32(smem);
+  const uint32_t full = smem0 + kThinRing, empty = full + 8 * kThinMost;
+  const uint32_t tfull = empty + 8 * kThinMost, sfull = tfull + 8, sums_in = sfull + 8;
+  const uint32_t sums = smem0 + kThinRing + 512;
+  const uint32_t scales = sums + kThinSums;   // [block of the run][row of A]
+  const uint32_t abort = smem_u32(&abort_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank()), C = a.split;
+  if (threadIdx.x == 0) {
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kThinRing);
+    for (int s = 0; s < 2 * kThinMost + 1; ++s) mbar_init(&bars[s], 1);
+    mbar_init(&bars[2 * kThinMost + 1], 2);     // scales: one arrival a scale warp
+    mbar_init(&bars[2 * kThinMost + 2], 4);     // sums: one arrival a warp of the CTA before
+    abort_flag = 0;
+    fence_barrier_init();
+    prefetch_map(&a.mapA[box_of(a.tile_rows)]);
+    prefetch_map(&a.mapW);
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, kCols);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  griddep_wait();
+  griddep_launch();
+
+  const int ntn = (a.width + 127) / 128;
+  const int nkb = (a.con + 127) / 128;
+  if (warp == 0) scan_groups(a, s_start, ntn, lane);
+  __syncthreads();
+  const int t = blockIdx.x / C;
+  if (t < s_start[a.G]) {   // the same for all CTAs of the cluster
+    const BTile ti = decode<128>(a, s_start, ntn, t);
+    const int per = (nkb + C - 1) / C;
+    const int kb0 = min(nkb, rank * per), n = min(nkb, kb0 + per) - kb0;   // this CTA's run (may be empty)
+    const int box = box_of(ti.nt);
+    if (warp == 0 && lane == 0) {
+      const uint32_t bytes = (16u << box) * 128u;
+      bool ok = static_cast<int>(bytes) <= a.a_slot && n * ti.nt <= 512;
+      if (!ok) {
+        atomicExch(&g_operator_error, kDevBadIndex);
+        abort_flag = 1;
+      }
+      int last[kThinMost];   // parity of the copy last issued to a stage
+      for (int s = 0; s < S; ++s) last[s] = -1;
+      for (int i = 0; ok && i < n; ++i) {
+        const int s = i % S;
+        const uint32_t ph = static_cast<uint32_t>(i / S) & 1u;
+        if (!bar_wait(empty + 8 * s, ph ^ 1u, abort)) { ok = false; break; }
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s),
+                     "r"(bytes + kWSlot) : "memory");
+        tma_load_2d(sA + s * a.a_slot, &a.mapA[box], (kb0 + i) * 128, ti.row0,
+                    reinterpret_cast<uint64_t*>(smem + kThinRing) + s);
+        if (TRANS) tma_load_3d(sW + s * kWSlot, &a.mapW, ti.n0, (kb0 + i) * 128, ti.g, full + 8 * s);
+        else tma_load_3d(sW + s * kWSlot, &a.mapW, (kb0 + i) * 128, ti.n0, ti.g, full + 8 * s);
+        last[s] = static_cast<int>(ph);
+      }
+      if (!ok)
+        for (int s = 0; s < S; ++s)
+          if (last[s] >= 0) mbar_wait_drain(reinterpret_cast<uint64_t*>(smem + kThinRing) + s, last[s], kDrain);
+    } else if (warp == 1) {
+      const bool issuer = elect_one();
+      // The weights are the M operand.
+      const uint32_t idesc = idesc_e4m3_f32(128, ti.nt) | (TRANS ? 1u << 15 : 0u);
+      const uint32_t tok_lo = (((smem0 + S * kWSlot) >> 4) & 0x3FFFu) | 1u << 16;
+      const uint32_t w_lo = ((smem0 >> 4) & 0x3FFFu) | (TRANS ? 16384u >> 4 : 1u) << 16;
+      int s = 0;
+      uint32_t ph = 0;
+      for (int i = 0; i < n; ++i) {
+        const bool ok = bar_wait(full + 8 * s, ph, abort);
+        if (!__all_sync(kFull, ok)) break;
+        tc_fence_after();
+        const uint32_t alo = w_lo + s * (kWSlot >> 4), blo = tok_lo + s * (static_cast<uint32_t>(a.a_slot) >> 4);
+        if (issuer) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_e4m3(tmem_base + i * ti.nt, (kDescHi << 32) | (alo + kk * (TRANS ? 4096 >> 4 : 2)),
+                      (kDescHi << 32) | (blo + kk * 2), idesc, kk != 0 ? 1u : 0u);
+          commit_one(empty + 8 * s);
+        }
+        __syncwarp();
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+      // Also when the run was cut short: the MMAs issued are done before TMEM goes.
+      if (issuer) commit_one(tfull);
+    } else if (warp == 2 || warp == 3) {
+      // fl(sa sw) of the run's blocks and the tile's rows (rows behind it: 0).
+      const int ob = ti.n0 / 128;
+      const float* pw = a.w_scale + ti.g * a.ws_g + ob * a.ws_o;
+      for (int j = threadIdx.x - 64; j < n * ti.nt; j += 64) {
+        const int b = j / ti.nt, r = j - b * ti.nt;
+        float v = 0.f;
+        if (r < ti.rows) v = __fmul_rn(a.a_scale[(kb0 + b) * a.ld_as + ti.row0 + r], pw[(kb0 + b) * a.ws_c]);
+        st_shared_f32(scales + 4 * j, v);
+      }
+      __syncwarp();
+      if (lane == 0) bar_arrive(sfull);
+    } else if (warp >= 4) {
+      const int q = warp & 3, row = q * 32 + lane;   // TMEM lane = weight row
+      const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+      bool ok = bar_wait(sfull, 0, abort) && bar_wait(tfull, 0, abort);
+      if (rank > 0) ok = ok && bar_wait_cluster(sums_in, 0, abort);
+      ok = __all_sync(kFull, ok);
+      tc_fence_after();
+      const int col = ti.n0 + row;
+      const uint32_t next = rank + 1 < C ? mapa_u32(sums, rank + 1) : 0u;
+      Out* out = static_cast<Out*>(a.out) + static_cast<size_t>(ti.row0) * a.ldo + col;
+      for (int c = 0; ok && c < ti.nt; c += 16) {
+        uint64_t acc[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          acc[i] = 0;
+        }
+        if (rank > 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ld_shared_pairs(sums + sum_at(row, c / 4 + i), acc[2 * i], acc[2 * i + 1]);
+        }
+        uint32_t v[2][16];
+        if (n > 0) tmem_ld<16>(tl + c, v[0]);
+        // Two blocks a turn, the second's load under the first's multiply-adds.
+        for (int b = 0; b < n; b += 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (b + h >= n) break;
+            tmem_wait<16>(v[h]);
+            if (b + h + 1 < n) tmem_ld<16>(tl + (b + h + 1) * ti.nt + c, v[h ^ 1]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint64_t lo, hi;
+              ld_shared_pairs(scales + ((b + h) * ti.nt + c + 4 * i) * 4, lo, hi);
+              fma2(acc[2 * i], pack2u(v[h][4 * i], v[h][4 * i + 1]), lo);
+              fma2(acc[2 * i + 1], pack2u(v[h][4 * i + 2], v[h][4 * i + 3]), hi);
+            }
+          }
+        }
+        if (rank + 1 < C) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(next + sum_at(row, c / 4 + i)), "l"(acc[2 * i]),
+                         "l"(acc[2 * i + 1])
+                         : "memory");
+        } else if (col < a.width) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 f = unpack2(acc[i / 2]);
+            const float x = i & 1 ? f.y : f.x;
+            if (c + i < ti.rows) {
+              if constexpr (sizeof(Out) == 2)
+                out[static_cast<size_t>(c + i) * a.ldo] = static_cast<Out>(pack_bf16x2(x, 0.f) & 0xFFFFu);
+              else
+                out[static_cast<size_t>(c + i) * a.ldo] = x;
+            }
+          }
+        }
+      }
+      // After a time-out the next CTA is told all the same; it has its own error
+      // to find, or passes on what it has: the error word says the output is not whole.
+      __syncwarp();
+      if (rank + 1 < C && lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(mapa_u32(sums_in, rank + 1))
+                     : "memory");
+      tc_fence_before();
+    }
+  }
+  // No CTA leaves while another may still write to it; TMEM is free of running MMAs:
+  // the sums' warps waited for them (or, after a time-out, this one does).
+  if (warp == 1 && t < s_start[a.G]) mbar_wait_drain(reinterpret_cast<uint64_t*>(smem + kThinRing) + 2 * kThinMost, 0, kDrain);
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kCols);
+  }
+}
+
 using Kernel = void (*)(BlockGemmArgs);
 Kernel kernel_of(bool transposed, bool f32) {
   if (transposed) return f32 ? k_block_gemm<1, float> : k_block_gemm<1, uint16_t>;
   return f32 ? k_block_gemm<0, float> : k_block_gemm<0, uint16_t>;
+}
+
+Kernel thin_kernel_of(bool transposed, bool f32) {
+  if (transposed) return f32 ? k_block_gemm_thin<1, float> : k_block_gemm_thin<1, uint16_t>;
+  return f32 ? k_block_gemm_thin<0, float> : k_block_gemm_thin<0, uint16_t>;
 }
 
 std::mutex g_mu;
@@ -743,6 +1005,8 @@ int block_gemm_pairs() {
     int c = 0;
     if (cudaOccupancyMaxActiveClusters(&c, fn, &cfg) != cudaSuccess) c = 0;
     n = std::min(n, c);
+    const void* thin = reinterpret_cast<const void*>(thin_kernel_of(v & 1, v & 2));
+    if (cudaFuncSetAttribute(thin, cudaFuncAttributeMaxDynamicSharedMemorySize, kThinSmem) != cudaSuccess) n = 0;
   }
   cudaGetLastError();
   if (n <= 0) return 0;
@@ -754,6 +1018,23 @@ int block_gemm_pairs() {
 cudaError_t launch_block_gemm(const BlockGemmArgs& a, int max_tiles, cudaStream_t s) {
   const int pairs = block_gemm_pairs();
   if (pairs <= 0) return cudaErrorInvalidConfiguration;
+  if (a.split > 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(max_tiles) * a.split);
+    cfg.blockDim = dim3(kThinThreads);
+    cfg.dynamicSmemBytes = kThinSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, thin_kernel_of(a.transposed != 0, a.out_f32 != 0), a);
+  }
   return launch_k(kernel_of(a.transposed != 0, a.out_f32 != 0), dim3(2 * std::min(pairs, max_tiles)), dim3(kThreads),
                   kSmem, s, true, a);
 }

@@ -260,7 +260,23 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   while (tr > 32 && tr / 2 >= rows_most) tr /= 2;
   auto tiles = [&](int rows) { return ntn * std::max<long long>((M + rows - 1) / rows, std::min(G, M)); };
   while (tr > 32 && tiles(tr) < pairs) tr /= 2;
-  const int per_cta = tr == 256 ? 128 : tr / 2;
+  // At most 32 rows, and too few tiles for the SMs: clusters of 2 or 4 CTAs share a
+  // tile's contraction (tiles of 128 columns).  Each CTA in the walk costs about
+  // 1.5 us, so 4 only for 32 blocks or more; 8 lost everywhere, as few clusters of 8
+  // fit the device at once.  The block sums of a CTA's run have to fit 512 TMEM
+  // columns.  Measured, us (pair tiles; 2; 4): M = 8, N = 4096, K = 7168: 20; 15.2;
+  // 13.3.  M = 32: 21.5; not; 17.5.  M = 16, N = 7168, K = 2048: 9.5; 7.9; 16.1.
+  const int thin_rows = M <= 16 ? 16 : 32;
+  const long long thin_tiles = (width + 127ll) / 128 * std::min(G, M);   // one a group with rows
+  const long long nkb = (con + 127ll) / 128;
+  int split = 0;
+  if (M <= 32 && nkb >= 8 && thin_tiles <= pairs) {
+    const bool four = thin_tiles * 4 <= 128;
+    split = four && (nkb >= 32 || (nkb + 1) / 2 * thin_rows > 512) ? 4 : 2;
+    if ((nkb + split - 1) / split * thin_rows > 512) split = 0;
+  }
+  if (split) tr = thin_rows;
+  const int per_cta = split ? tr : (tr == 256 ? 128 : tr / 2);
   int boxes = 1;
   while ((16 << (boxes - 1)) < per_cta) ++boxes;
   for (int b = 0; b < boxes; ++b)
@@ -273,6 +289,7 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   g.width = width;
   g.transposed = transposed;
   g.tile_rows = tr;
+  g.split = split;
   g.a_slot = (16 << (boxes - 1)) * 128;
   g.a_scale = a_scale;
   g.ld_as = ld_as;
@@ -285,8 +302,8 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   g.ldo = ldo;
   g.out_f32 = out_dtype == MOE_DTYPE_F32;
   g.out_vec = al(out, 16) && pitch16(ldo, osize);
-  const long long max_tiles = ntn * ((M + tr - 1) / tr + G);
-  return status(launch_block_gemm(g, static_cast<int>(std::min<long long>(max_tiles, pairs)),
+  const long long max_tiles = split ? thin_tiles : std::min<long long>(ntn * ((M + tr - 1) / tr + G), pairs);
+  return status(launch_block_gemm(g, static_cast<int>(max_tiles),
                                   static_cast<cudaStream_t>(stream)));
 }
 

@@ -87,6 +87,7 @@ struct BlockGemmArgs {
   int tile_rows;          // rows per tile: 256 (full tiles with the rows as the MMA's M), or fewer
                           // (every tile with the weights as M)
   int a_slot;             // A bytes per stage
+  int split;              // 0, or CTAs that share a tile's contraction (products of few tiles)
   const float* a_scale;   // [con / 128, ld_as]
   long long ld_as;
   const float* w_scale;   // group g, output block o, contraction block c at g * ws_g + o * ws_o + c * ws_c

@@ -765,3 +765,34 @@ def test_binding_refuses(torch, moe):
         with pytest.raises(moe.MoEError) as err:
             call()
         assert err.value.status == status
+
+
+# Shapes with too few tiles for the device, whose contraction is divided over the
+# CTAs of a cluster: both splits (2, 4), runs of unequal length, rows to the last of a
+# tile, and shapes just outside.
+@pytest.mark.parametrize("M,N,K", [(1, 128, 16), (8, 256, 384), (16, 1000, 1040), (17, 4096, 1152), (33, 130, 2064),
+                                   (32, 512, 4096), (30, 384, 1152), (8, 4096, 2048), (5, 8000, 640), (8, 1024, 7168),
+                                   (32, 256, 8192), (32, 256, 9216)])
+@pytest.mark.parametrize("transposed", [False, True])
+def test_matmul_of_few_tiles(torch, moe, M, N, K, transposed):
+    N = -(-N // 16) * 16 if transposed else N
+    a, sa, w, sw = _operands(torch, moe, M + N + K, M, N, K, transposed=transposed)
+    _check_matmul(torch, moe, a, sa, w, sw, transposed=transposed, dtype="f32" if M % 2 else "bf16")
+
+
+@pytest.mark.parametrize("off", [[0, 3, 3, 20], [2, 2, 18, 30], [0, 0, 0, 0], [0, 30, 30, 30], [0, 64, 129, 130]], ids=str)
+def test_matmul_of_few_tiles_grouped(torch, moe, off):
+    M = max(off[-1], 1) + 2
+    a, sa, w, sw = _operands(torch, moe, M, M, 200, 1168, G=3)
+    _check_matmul(torch, moe, a, sa, w, sw, off)
+
+
+@pytest.mark.parametrize("K", [384, 2064, 7168])
+def test_matmul_of_few_tiles_has_the_same_bits(torch, moe, K):
+    """Rows alone, in batches whose contraction is divided, and in one that is not."""
+    a, sa, w, sw = _operands(torch, moe, 9, 3000, 1024, K)
+    whole = moe.matmul_fp8(a, sa, w, sw, out_dtype=torch.float32)
+    for lo, hi in ((0, 1), (7, 23), (100, 133), (500, 564), (1000, 1128), (2000, 2300)):
+        part = moe.matmul_fp8(a[lo:hi].contiguous(), sa[:, lo:hi].contiguous(), w, sw, out_dtype=torch.float32)
+        assert torch.equal(part.view(torch.int32), whole[lo:hi].view(torch.int32)), (lo, hi)
+    assert moe.operator_error() == moe.MOE_OK
