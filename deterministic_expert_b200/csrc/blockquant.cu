@@ -116,15 +116,13 @@ __device__ __forceinline__ uint2 codes8_bf16(const float (&v)[8], const BlockSca
     x[i] = pair(v[2 * i], v[2 * i + 1]);
     q[i] = mul2(x[i], f2);
   }
-  uint2 c = make_uint2(e4m3x2(q[0]) | e4m3x2(q[1]) << 16, e4m3x2(q[2]) | e4m3x2(q[3]) << 16);
   if (b.rem == 0.f) {
-    const uint64_t s2 = pair(-b.s, -b.s);
+    // q - (q s - x) f: with a zero remainder (always +0) a zero keeps its sign.
+    const uint64_t s2 = pair(b.s, b.s), one = pair(-1.f, -1.f), n2 = pair(-f, -f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fma2(fma2(q[i], s2, x[i]), f2, q[i]);
-    // (The correction of a zero is a zero of either sign: signs stay.)
-    c.x = (c.x & 0x80808080u) | e4m3x2(q[0]) | e4m3x2(q[1]) << 16;
-    c.y = (c.y & 0x80808080u) | e4m3x2(q[2]) | e4m3x2(q[3]) << 16;
+    for (int i = 0; i < 4; ++i) q[i] = fma2(fma2(q[i], s2, mul2(x[i], one)), n2, q[i]);
   }
+  const uint2 c = make_uint2(e4m3x2(q[0]) | e4m3x2(q[1]) << 16, e4m3x2(q[2]) | e4m3x2(q[3]) << 16);
   return c;
 }
 
@@ -237,10 +235,12 @@ __device__ __forceinline__ void glu_parts(float g, float u, const QuantArgs& a, 
 // block and every load and store of the eight lanes is one segment.  A CTA of 256
 // threads takes 32 rows (their scales of a block are one 128-byte segment) and
 // walks their blocks, U at a time so that their loads are in flight together.
-// Bound by memory: every element is read once and its code written once.
+// Bound by memory: every element is read once and its code written once.  24576 bf16
+// rows of 2048: 25.4 us (6.0 TB/s; two blocks at a time 27.3), and 24.7 us gathered
+// from 4096 rows, which then come through L2.
 constexpr int kRowsPerCta = 32;
 template <int KIND>
-constexpr int kUnroll = KIND == kQuantBf16 ? 2 : 1;
+constexpr int kUnroll = KIND == kQuantBf16 ? 4 : 1;
 
 template <int KIND, int GLU = kSwiglu>
 __global__ void __launch_bounds__(256) k_quant_blocks(const QuantArgs a) {
