@@ -14,6 +14,9 @@ using namespace moe;
 
 namespace {
 
+// Rows (and columns) that the kernels' 32-bit indexes can round up to whole tiles.
+constexpr int kMost = INT_MAX - 256;
+
 bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool dtype_ok(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
 size_t dtype_size(int d) { return d == MOE_DTYPE_BF16 ? 2 : 4; }
@@ -57,14 +60,14 @@ int check_route(const moe_route_config* c, int T) {
     return MOE_EINVAL;
   if (c->E > kRouteMaxE || c->k > kRouteMaxK || c->k > c->E || c->n_groups > 32 || c->E % c->n_groups)
     return MOE_EUNSUPPORTED;
-  if (static_cast<long long>(T) * c->k > INT_MAX) return MOE_EUNSUPPORTED;
+  if (static_cast<long long>(T) * c->k > kMost) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
 int check_glu(const moe_glu_config* c) {
   if (!c) return MOE_EINVAL;
   if (c->activation == MOE_ACT_SWIGLU)
-    return !std::isnan(c->gate_clamp_max) && c->up_clamp >= 0.f ? MOE_OK : MOE_EINVAL;
+    return c->gate_clamp_max > -INFINITY && c->up_clamp >= 0.f ? MOE_OK : MOE_EINVAL;
   if (c->activation == MOE_ACT_SITU_GLU)
     return c->situ_beta_gate > 0.f && std::isfinite(c->situ_beta_gate) && c->situ_beta_up > 0.f &&
                    std::isfinite(c->situ_beta_up)
@@ -143,7 +146,7 @@ int moe_route_backward(const moe_route_config* cfg, int T, const void* logits, l
 int moe_group_rows(int T, int k, int E, const int32_t* idx, int32_t* offsets, int32_t* token_of_row,
                    int32_t* row_of_slot, void* stream) {
   if (T < 0 || k <= 0 || E <= 0 || !offsets || !al(offsets, 4)) return MOE_EINVAL;
-  if (E > kRouteMaxE || static_cast<long long>(T) * k > INT_MAX) return MOE_EUNSUPPORTED;
+  if (E > kRouteMaxE || static_cast<long long>(T) * k > kMost) return MOE_EUNSUPPORTED;
   if (T > 0 && (!idx || !token_of_row || !row_of_slot || !al(idx, 4) || !al(token_of_row, 4) || !al(row_of_slot, 4)))
     return MOE_EINVAL;
   // T = 0 still writes the offsets (all 0).
@@ -154,7 +157,7 @@ int moe_quantize_rows_fp8(int rows, int K, const void* x, int dtype, long long l
                           const int32_t* token_of_row, const int32_t* n_rows, uint8_t* codes, float* scales,
                           long long ld_s, void* stream) {
   if (rows < 0 || K <= 0 || !dtype_ok(dtype) || src_rows < 0) return MOE_EINVAL;
-  if (K % 16 || K > (1 << 20)) return MOE_EUNSUPPORTED;
+  if (K % 16 || K > (1 << 20) || rows > kMost) return MOE_EUNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!x || !codes || !scales || ld < K || ld_s < rows || !al(x, 16) || !pitch16(ld, dtype_size(dtype)) ||
       !al(codes, 16) || !al(scales, 4) || !al(token_of_row, 4) || !al(n_rows, 4))
@@ -176,7 +179,7 @@ int moe_quantize_rows_fp8(int rows, int K, const void* x, int dtype, long long l
 
 int moe_quantize_weights_fp8(int G, int N, int K, const moe_bf16* w, uint8_t* codes, float* scales, void* stream) {
   if (G < 0 || N <= 0 || K <= 0) return MOE_EINVAL;
-  if (K % 16 || G > 65535 || (N + 127) / 128 > 65535) return MOE_EUNSUPPORTED;
+  if (K % 16 || K > kMost || G > 65535 || (N + 127ll) / 128 > 65535) return MOE_EUNSUPPORTED;
   if (G == 0) return MOE_OK;
   if (!w || !codes || !scales || !al(w, 16) || !al(codes, 16) || !al(scales, 4)) return MOE_EINVAL;
   return status(launch_quant_weights_block(w, codes, scales, G, N, K, static_cast<cudaStream_t>(stream)));
@@ -187,7 +190,7 @@ static int glu_args(const moe_glu_config* cfg, int rows, int I, const moe_bf16* 
   const int v = check_glu(cfg);
   if (v != MOE_OK) return v;
   if (rows < 0 || I <= 0) return MOE_EINVAL;
-  if (I % 16 || I > (1 << 19)) return MOE_EUNSUPPORTED;
+  if (I % 16 || I > (1 << 19) || rows > kMost) return MOE_EUNSUPPORTED;
   if (rows > 0 && (!gu || !codes || !scales || ld < 2ll * I || ld_s < rows || !al(gu, 16) || !pitch16(ld, 2) ||
                    !al(codes, 16) || !al(scales, 4) || !al(n_rows, 4)))
     return MOE_EINVAL;
@@ -237,27 +240,28 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   if (G <= 0 || M < 0 || N <= 0 || K <= 0 || !dtype_ok(out_dtype) || (transposed != 0 && transposed != 1) ||
       (G > 1 && M > 0 && !offsets))
     return MOE_EINVAL;
-  const int most = INT_MAX - 256;
-  if (K % 16 || (transposed && N % 16) || G > kMatmulMaxGroups || M > most || N > most || K > most)
+  if (K % 16 || (transposed && N % 16) || G > kMatmulMaxGroups || M > kMost || N > kMost || K > kMost)
     return MOE_EUNSUPPORTED;
   if (M == 0) return MOE_OK;
   const int con = transposed ? N : K, width = transposed ? K : N;
   const size_t osize = dtype_size(out_dtype);
+  const long long ntn = (width + 255) / 256;
+  // Rows per tile.  256 rows run as full tiles; where groups are small (at most a
+  // quarter of that on average, so that few have a second tile) or, below, the tiles
+  // too few for the device's CTA pairs, less.  No choice changes a result's bits.
+  const long long avg = (static_cast<long long>(M) + G - 1) / G;
+  const long long rows_most = std::min<long long>(M, 4 * avg);
+  int tr = 256;
+  while (tr > 32 && tr / 2 >= rows_most) tr /= 2;
+  // Tiles are counted in 32 bits on the device, whatever the offsets hold there.
+  if (static_cast<double>(ntn) * ((M + tr - 1ll) / tr) * G > 0x7fff0000) return MOE_EUNSUPPORTED;
   if (!a || !a_scale || !w || !w_scale || !out || ld_as < M || ldo < width || !al(a, 16) || !al(w, 16) ||
       !al(a_scale, 4) || !al(w_scale, 4) || !al(out, osize) || !al(offsets, 4))
     return MOE_EINVAL;
   const int pairs = block_gemm_pairs();
   if (pairs <= 0) return status(cudaErrorInvalidConfiguration);
 
-  const long long ntn = (width + 255) / 256;
   BlockGemmArgs g = {};
-  // Rows per tile.  256 rows run as full tiles; where groups are small (at most a
-  // quarter of that on average, so that few have a second tile) or the tiles too
-  // few for the device's CTA pairs, less.  No choice changes a result's bits.
-  const long long avg = (static_cast<long long>(M) + G - 1) / G;
-  const long long rows_most = std::min<long long>(M, 4 * avg);
-  int tr = 256;
-  while (tr > 32 && tr / 2 >= rows_most) tr /= 2;
   auto tiles = [&](int rows) { return ntn * std::max<long long>((M + rows - 1) / rows, std::min(G, M)); };
   while (tr > 32 && tiles(tr) < pairs) tr /= 2;
   // At most 32 rows, and too few tiles for the SMs: clusters of 2 or 4 CTAs share a
@@ -311,7 +315,7 @@ int moe_combine_rows(int T, int k, int D, int rows, const void* y, int y_dtype, 
                      const int32_t* row_of_slot, const float* w, const moe_bf16* addend, void* out, int out_dtype,
                      void* stream) {
   if (T < 0 || k <= 0 || D <= 0 || rows < 0 || !dtype_ok(y_dtype) || !dtype_ok(out_dtype)) return MOE_EINVAL;
-  if (D % 8 || k > kRouteMaxK || D > (1 << 20)) return MOE_EUNSUPPORTED;
+  if (D % 8 || k > kRouteMaxK || D > (1 << 20) || T > kMost || rows > kMost) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!row_of_slot || !out || (rows > 0 && !y) || ld_y < D || !al(y, 16) || !pitch16(ld_y, dtype_size(y_dtype)) ||
       !al(row_of_slot, 4) || !al(w, 4) || !al(addend, 16) || !al(out, 16))
@@ -335,7 +339,7 @@ int moe_combine_rows_backward(int T, int k, int D, int rows, const moe_bf16* dou
                               long long ld_y, const int32_t* row_of_slot, const float* w, void* dy, float* dw,
                               void* stream) {
   if (T < 0 || k <= 0 || D <= 0 || rows < 0 || !dtype_ok(y_dtype)) return MOE_EINVAL;
-  if (D % 8 || k > kRouteMaxK || D > (1 << 20)) return MOE_EUNSUPPORTED;
+  if (D % 8 || k > kRouteMaxK || D > (1 << 20) || T > kMost || rows > kMost) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dout || !row_of_slot || (rows > 0 && (!dy || (dw && !y))) || ld_y < D || !al(dout, 16) || !al(y, 16) ||
       !pitch16(ld_y, dtype_size(y_dtype)) || !al(row_of_slot, 4) || !al(w, 4) || !al(dy, 16) || !al(dw, 4))

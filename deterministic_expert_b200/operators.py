@@ -126,11 +126,16 @@ _I32, _F32, _BF16 = (torch.int32,), (torch.float32,), (torch.bfloat16,)
 
 
 @functools.lru_cache(maxsize=256)
+def _route_struct(E, k, dtype, softmax, n_groups, topk_groups, group_top, renormalize, routed_scale):
+    return moe_route_config(E, k, _moe.ROUTER_SOFTMAX if softmax else _moe.ROUTER_SIGMOID_BIAS, n_groups, topk_groups,
+                            group_top, renormalize, routed_scale, _DTYPES[dtype])
+
+
 def _route_config(E, k, dtype, scores, n_groups, topk_groups, group_top, renormalize, routed_scale):
-    _need(scores in ("softmax", "sigmoid"), f"scores: expected 'softmax' or 'sigmoid', got {scores!r}")
-    return moe_route_config(E, int(k), _moe.ROUTER_SOFTMAX if scores == "softmax" else _moe.ROUTER_SIGMOID_BIAS,
-                            int(n_groups), int(topk_groups), int(group_top), 1 if renormalize else 0,
-                            float(routed_scale), _DTYPES[dtype])
+    _need(scores == "softmax" or scores == "sigmoid", f"scores: expected 'softmax' or 'sigmoid', got {scores!r}")
+    # Plain numbers only: the structures are kept by value.
+    return _route_struct(E, int(k), dtype, scores == "softmax", int(n_groups), int(topk_groups), int(group_top),
+                         1 if renormalize else 0, float(routed_scale))
 
 
 def route(logits, k: int, *, scores: str = "softmax", bias=None, n_groups: int = 1, topk_groups: int = 1,
@@ -260,10 +265,13 @@ def quantize_weights_fp8(w, *, out_codes=None, out_scales=None, stream=None):
     return out_codes, out_scales
 
 
-@functools.lru_cache(maxsize=256)
+_glu_struct = functools.lru_cache(maxsize=256)(moe_glu_config)
+
+
 def _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up):
-    return moe_glu_config(int(activation), float(gate_clamp_max), float(up_clamp), float(situ_beta_gate),
-                          float(situ_beta_up))
+    # Plain numbers only: the structures are kept by value.
+    return _glu_struct(int(activation), float(gate_clamp_max), float(up_clamp), float(situ_beta_gate),
+                       float(situ_beta_up))
 
 
 def _gate_up(gu):
@@ -397,4 +405,5 @@ def operator_error(device=None, stream=None) -> int:
     the error word of matmul_fp8.  Synchronises the stream."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
-        return int(_fn("moe_get_operator_error")(_raw_stream(dev.index) if stream is None else _handle(stream)))
+        s = _raw_stream(torch.cuda.current_device()) if stream is None else _handle(stream)
+        return int(_fn("moe_get_operator_error")(s))

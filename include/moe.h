@@ -545,6 +545,8 @@ int moe_peer_barrier(int world, int rank, uint32_t* const* flags, uint32_t epoch
  * Matrices are row-major; rows are densely packed unless a row pitch ("ld", in
  * elements) is given.  Unless noted a pointer to 8- or 16-byte vectors must be
  * 16-byte aligned.  Rows = 0 (or T = 0) returns MOE_OK and launches nothing.
+ * Rows, tokens and slots (T k) number at most 2^31 - 257; D and K of the
+ * row-wise operators at most 2^20.
  * Errors: MOE_EINVAL (NULL, misaligned, negative size, bad enum),
  * MOE_EUNSUPPORTED (a size outside the limits given), MOE_ECUDA (launch).
  * ------------------------------------------------------------------------ */
@@ -589,7 +591,7 @@ int moe_route_backward(const moe_route_config* cfg, int T, const void* logits, l
  * inside an expert by token, then slot.  offsets [E + 1]: expert e has rows
  * offsets[e] .. offsets[e + 1] - 1; token_of_row [T k]: a row's token, -1 behind
  * the last row; row_of_slot [T, k]: a slot's row, -1 for an index outside [0, E).
- * 1 <= E <= 1024, 1 <= k, T k < 2^31. */
+ * 1 <= E <= 1024, 1 <= k.  T = 0 writes the offsets. */
 int moe_group_rows(int T, int k, int E, const int32_t* idx, int32_t* offsets, int32_t* token_of_row,
                    int32_t* row_of_slot, void* stream);
 
@@ -615,7 +617,7 @@ int moe_quantize_weights_fp8(int G, int N, int K, const moe_bf16* w, uint8_t* co
 
 typedef struct moe_glu_config {
   int activation;        /* moe_activation                                              */
-  float gate_clamp_max;  /* SwiGLU: as in moe_config (+INF = off)                       */
+  float gate_clamp_max;  /* SwiGLU: as in moe_config (> -INF; +INF = off)               */
   float up_clamp;        /* SwiGLU: as in moe_config (>= 0; +INF = off)                 */
   float situ_beta_gate;  /* SiTU-GLU (> 0, finite)                                      */
   float situ_beta_up;    /* SiTU-GLU (> 0, finite)                                      */
@@ -646,7 +648,8 @@ int moe_glu_backward_quantize_fp8(const moe_glu_config* cfg, int rows, int I, co
  * fma(block sum, a_scale * w_scale, sum), and the sum is rounded once to
  * out_dtype (moe_dtype).  out [M, ldo].
  * Limits: K a multiple of 16, and N too when transposed; G <= 1024;
- * M, N, K < 2^31 - 256.  out may start and step at any alignment of its type
+ * M, N, K at most 2^31 - 257, and G ceil(M / tile rows) ceil(columns / 256) tiles
+ * (of 32 to 256 rows, more rows where groups are larger) below 2^31.  out may start and step at any alignment of its type
  * (16-byte aligned rows store faster). */
 int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, int K, const uint8_t* a,
                    const float* a_scale, long long ld_as, const uint8_t* w, const float* w_scale, void* out,

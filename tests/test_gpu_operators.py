@@ -796,3 +796,88 @@ def test_matmul_of_few_tiles_has_the_same_bits(torch, moe, K):
         part = moe.matmul_fp8(a[lo:hi].contiguous(), sa[:, lo:hi].contiguous(), w, sw, out_dtype=torch.float32)
         assert torch.equal(part.view(torch.int32), whole[lo:hi].view(torch.int32)), (lo, hi)
     assert moe.operator_error() == moe.MOE_OK
+
+
+# ------------------------------------------------ offsets past 32 bits
+def _large(torch, rows, cols):
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator(device="cuda").manual_seed(rows))
+    return x
+
+
+def test_offsets_past_32_bits_in_rows(torch, moe):
+    """Rows behind the 2^31st element: the bits of the same rows in a small call."""
+    R_, K = 270_000, 8192
+    tail = slice(R_ - 200, R_)
+    x = _large(torch, R_, K)
+    q, s = moe.quantize_rows_fp8(x)
+    q2, s2 = moe.quantize_rows_fp8(x[tail])
+    assert torch.equal(q[tail], q2) and torch.equal(s[:, tail], s2)
+    w, sw = moe.quantize_weights_fp8(_randn(torch, 3, K, K, dtype="bf16"))
+    w2, sw2 = w[:, :K // 64].contiguous(), sw[:, :1].contiguous()          # 128 columns: a short contraction
+    out = moe.matmul_fp8(q[:, :128].contiguous(), s[:1].contiguous(), w2, sw2, out_dtype=torch.float32)
+    want = moe.matmul_fp8(q2[:, :128].contiguous(), s2[:1].contiguous(), w2, sw2, out_dtype=torch.float32)
+    assert torch.equal(out[tail], want)
+    del out
+    out = moe.matmul_fp8(q, s, w[:256].contiguous(), sw[:2].contiguous())
+    assert torch.equal(out[tail], moe.matmul_fp8(q2, s2.contiguous(), w[:256].contiguous(), sw[:2].contiguous()))
+    del out
+    h, hs = moe.glu_quantize_fp8(x)
+    h2, hs2 = moe.glu_quantize_fp8(x[tail])
+    assert torch.equal(h[tail], h2) and torch.equal(hs[:, tail], hs2)
+    del h
+    d = _large(torch, 200, K // 2)
+    dh = torch.zeros(R_, K // 2, dtype=torch.bfloat16, device="cuda")
+    dh[tail] = d
+    g, gs = moe.glu_backward_quantize_fp8(x, dh, out_codes=q, out_scales=s)
+    g2, gs2 = moe.glu_backward_quantize_fp8(x[tail], d)
+    assert torch.equal(g[tail], g2) and torch.equal(gs[:, tail], gs2)
+    del dh
+    slots = torch.arange(R_ - 200, R_, dtype=torch.int32, device="cuda").view(100, 2)
+    wt = torch.rand(100, 2, device="cuda")
+    assert torch.equal(moe.combine_rows(x, slots, wt), moe.combine_rows(x[tail], slots - (R_ - 200), wt))
+    dout = _large(torch, 100, K)
+    dy, dw = moe.combine_rows_backward(dout, x, slots, wt)
+    dy2, dw2 = moe.combine_rows_backward(dout, x[tail], slots - (R_ - 200), wt)
+    assert torch.equal(dy[tail], dy2) and torch.equal(dw, dw2)
+    assert moe.operator_error("cuda") == moe.MOE_OK
+
+
+def test_offsets_past_32_bits_in_weights_and_logits(torch, moe):
+    G, N, K = 9, 16384, 16384
+    w = torch.empty(G, N, K, dtype=torch.bfloat16, device="cuda")
+    w.normal_(generator=torch.Generator(device="cuda").manual_seed(5))
+    q, s = moe.quantize_weights_fp8(w)
+    last, slast = moe.quantize_weights_fp8(w[-1])
+    assert torch.equal(q[-1], last) and torch.equal(s[-1], slast)
+    del w
+    a, sa = moe.quantize_rows_fp8(_randn(torch, 1, 20, K, dtype="bf16"))
+    off = torch.tensor([0] * G + [20], dtype=torch.int32, device="cuda")
+    for transposed in (False, True):
+        assert torch.equal(moe.matmul_fp8(a, sa, q, s, offsets=off, transposed=transposed),
+                           moe.matmul_fp8(a, sa, last, slast, transposed=transposed))
+    del q
+    T, E, k = 2_200_000, 1024, 4
+    logits = _large(torch, T, E)
+    tail = slice(T - 100, T)
+    idx, wt = moe.route(logits, k, renormalize=True)
+    idx2, wt2 = moe.route(logits[tail], k, renormalize=True)
+    assert torch.equal(idx[tail], idx2) and torch.equal(wt[tail], wt2)
+    dl = moe.route_backward(logits, idx, wt)
+    assert torch.equal(dl[tail], moe.route_backward(logits[tail], idx2, wt2))
+
+
+def test_products_on_two_streams_at_once(torch, moe):
+    """Products that divide a contraction over clusters beside ones of whole tiles."""
+    few = _operands(torch, moe, 1, 8, 2048, 4096)
+    many = _operands(torch, moe, 2, 700, 2048, 1024)
+    want = [moe.matmul_fp8(*few), moe.matmul_fp8(*many)]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(60):
+        with torch.cuda.stream(streams[i % 3]):
+            got.append(moe.matmul_fp8(*(few if i % 2 == 0 else many)))
+    torch.cuda.synchronize()
+    assert moe.operator_error() == moe.MOE_OK
+    assert all(torch.equal(g, want[i % 2]) for i, g in enumerate(got))

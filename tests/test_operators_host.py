@@ -110,6 +110,45 @@ def test_matmul_refuses():
     assert mm(M=0, a=None) == moe.MOE_OK
 
 
+def test_sizes_that_pass_32_bits_are_refused():
+    most, no = (1 << 31) - 257, moe.MOE_EUNSUPPORTED
+    cfg = _cfg(k=1)
+    assert _route(cfg, T=most + 1) == no and _route(_cfg(k=2), T=most) == no
+    assert ops._fn("moe_route_backward")(ctypes.byref(cfg), most + 1, FAKE, 64, FAKE, FAKE, FAKE, 64, None) == no
+    assert ops._fn("moe_group_rows")(most + 1, 1, 8, FAKE, FAKE, FAKE, FAKE, None) == no
+    q = ops._fn("moe_quantize_rows_fp8")
+    assert q(most + 1, 128, FAKE, 0, 128, 4, None, None, FAKE, FAKE, most + 1, None) == no
+    assert q(4, (1 << 20) + 16, FAKE, 0, 1 << 21, 4, None, None, FAKE, FAKE, 4, None) == no
+    w = ops._fn("moe_quantize_weights_fp8")
+    assert w(1, (1 << 31) - 1, 128, FAKE, FAKE, FAKE, None) == no
+    assert w(1, 128, (1 << 31) - 16, FAKE, FAKE, FAKE, None) == no
+    inf = float("inf")
+    glu = ops.moe_glu_config(0, inf, inf, 4.0, 25.0)
+    assert ops._fn("moe_glu_quantize_fp8")(ctypes.byref(glu), most + 1, 128, FAKE, 256, None, FAKE, FAKE, most + 1,
+                                           None) == no
+    glu.gate_clamp_max = -inf          # would clamp every gate away
+    assert ops._fn("moe_glu_quantize_fp8")(ctypes.byref(glu), 4, 128, FAKE, 256, None, FAKE, FAKE, 4,
+                                           None) == moe.MOE_EINVAL
+    mm = ops._fn("moe_matmul_fp8")
+    for M, N, K, G in ((1 << 28, 1 << 28, 16, 1), (1 << 24, 1 << 20, 128, 1024), (most, most, 16, 1), (4, most + 1, 16, 1)):
+        assert mm(0, G, FAKE, M, N, K, FAKE, FAKE, M, FAKE, FAKE, FAKE, 0, N, None) == no, (M, N, K, G)
+    assert ops._fn("moe_combine_rows")(most + 1, 1, 64, 8, FAKE, 0, 64, FAKE, None, None, FAKE, 0, None) == no
+    assert ops._fn("moe_combine_rows")(4, 1, 64, most + 1, FAKE, 0, 64, FAKE, None, None, FAKE, 0, None) == no
+    assert ops._fn("moe_combine_rows_backward")(most + 1, 1, 64, 8, FAKE, FAKE, 0, 64, FAKE, None, FAKE, FAKE,
+                                                None) == no
+
+
+def test_configurations_are_kept_by_value():
+    scale, bound = torch.tensor(1.5), torch.tensor(7.0)
+    first = ops._route_config(8, 2, torch.float32, "sigmoid", 1, 1, 2, False, scale).routed_scale
+    clamp = ops._glu_config(0, bound, bound, 4.0, 25.0).up_clamp
+    scale.fill_(2.5)
+    bound.fill_(3.0)
+    assert first == 1.5 and clamp == 7.0
+    assert ops._route_config(8, 2, torch.float32, "sigmoid", 1, 1, 2, False, scale).routed_scale == 2.5
+    assert ops._glu_config(0, bound, bound, 4.0, 25.0).up_clamp == 3.0
+
+
 def test_combine_refuses():
     f, b = ops._fn("moe_combine_rows"), ops._fn("moe_combine_rows_backward")
 
