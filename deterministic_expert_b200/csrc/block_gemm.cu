@@ -683,6 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         // cover 128-byte row segments (chunk m of row r at m ^ (r & 7)).
         const int r0 = static_cast<int>(rank) * 128 + q * 32;
         const int col0 = ti.n0 + half * 128;
+        const int rows = ti.rows - r0;
+        const bool fast = a.out_vec && col0 + 128 <= a.width;
+        Out* base = out + static_cast<size_t>(ti.row0 + r0 + (lane >> 3)) * a.ldo + col0 + (lane & 7) * kPer;
+        const size_t step = static_cast<size_t>(a.ldo) * 4;
 #pragma unroll
         for (int p = 0; p < 128 / kSeg; ++p) {
           __syncwarp();
@@ -701,21 +705,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
             *reinterpret_cast<uint4*>(stage_w + lane * 128 + ((m ^ (lane & 7)) << 4)) = u;
           }
           __syncwarp();
+          Out* dst = base + p * kSeg;
+          if (fast) {
 #pragma unroll
-          for (int it = 0; it < 8; ++it) {
-            const int r = it * 4 + (lane >> 3), ch = lane & 7;
-            const int col = col0 + p * kSeg + ch * kPer;
-            const uint4 u = *reinterpret_cast<const uint4*>(stage_w + r * 128 + ((ch ^ (r & 7)) << 4));
-            if (r0 + r >= ti.rows) continue;
-            Out* dst = out + static_cast<size_t>(ti.row0 + r0 + r) * a.ldo + col;
-            if (a.out_vec && col + kPer <= a.width) {
-              *reinterpret_cast<uint4*>(dst) = u;
-            } else {
+            for (int it = 0; it < 8; ++it, dst += step) {
+              const int r = it * 4 + (lane >> 3), ch = lane & 7;
+              const uint4 u = *reinterpret_cast<const uint4*>(stage_w + r * 128 + ((ch ^ (r & 7)) << 4));
+              if (r < rows) *reinterpret_cast<uint4*>(dst) = u;
+            }
+          } else {
+            const int col = col0 + p * kSeg + (lane & 7) * kPer;
+            for (int it = 0; it < 8; ++it, dst += step) {
+              const int r = it * 4 + (lane >> 3), ch = lane & 7;
               union { uint4 u; Out e[kPer]; } x;
-              x.u = u;
+              x.u = *reinterpret_cast<const uint4*>(stage_w + r * 128 + ((ch ^ (r & 7)) << 4));
+              if (r >= rows) continue;
+              if (a.out_vec && col + kPer <= a.width) {
+                *reinterpret_cast<uint4*>(dst) = x.u;
+              } else {
 #pragma unroll
-              for (int z = 0; z < kPer; ++z)
-                if (col + z < a.width) dst[z] = x.e[z];
+                for (int z = 0; z < kPer; ++z)
+                  if (col + z < a.width) dst[z] = x.e[z];
+              }
             }
           }
         }
