@@ -14,9 +14,14 @@
 // shape, operand roles, group or batch, so its bits depend on its own row alone.
 //
 // Bound: 128 rows x 256 columns of a CTA take 512 tensor-pipe cycles a block at
-// the nominal rate; reading P_b back (32 columns a load) and its 32768
-// multiply-adds (packed in pairs) take the epilogue warps about half of that when
-// they overlap, so two accumulator buffers of 256 TMEM columns keep both busy.
+// the nominal rate, about 680 with both operands coming from shared memory.  Reading
+// P_b back takes another 512 (128 KB at TMEM's rate) plus the latencies of commit,
+// first load and release; the two accumulator buffers of 256 TMEM columns overlap the
+// two, and the round trip of a buffer through both, about 880 cycles a block, is what
+// bounds large products: 8192 x 4096 x 7168 in 219 us, 2190 TFLOP/s, the tensor pipe
+// busy half of the time.  A tile's store costs 1.3 us (all SMs write at once) and its
+// start 0.5 us, which short contractions feel.  Few rows a group are bound by the
+// weights' stream: 384 rows over 64 groups of 2816 x 2048 at 5.9-6.1 TB/s.
 //
 // A CTA pair (cta_group::2) works on 256 rows of one operand and up to 256 of the
 // other:
