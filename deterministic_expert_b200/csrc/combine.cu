@@ -49,7 +49,8 @@ struct Eight<float> {
 // One CTA per token.  Its slots' rows and weights are read once into shared memory;
 // a thread then takes 8 columns at a time, kSlotsAtOnce slots' loads issued before
 // they are added, in slot order.
-// Bound by memory: k rows read, one written.
+// Bound by memory: k rows read, one written; T = 8192, k = 8, D = 7168 bf16 in 155 us,
+// 6.8 TB/s.
 constexpr int kSlotsAtOnce = 8;
 
 // Threads for D columns, 8 a thread: as few passes as 256 threads need, evenly.
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(256) k_combine_rows(const CombineArgs a) {
 // One CTA per token: a thread takes 8 columns of dout at a time, reads its slots'
 // y, writes their dy and adds to their dot products; the products are summed over
 // the CTA in a fixed tree.
-// Bound by memory: k rows read, k rows written.
+// Bound by memory: k rows read, k rows written; T = 4096, k = 6, D = 2048 bf16 in
+// 37.8 us, 5.8 TB/s.  Two slots at a time: more take registers, and with them resident CTAs.
 constexpr int kSlotsBack = 2;
 
 template <typename Y>
