@@ -446,6 +446,21 @@ def test_matmul_output_strides(torch, moe, M, dtype, ld, shift):
     assert (buf[shift:].view(M, ld)[:, 290:] == 5).all() and (buf[:shift] == 5).all()
 
 
+@pytest.mark.parametrize("N", [1, 2, 63, 64, 65, 127, 129, 191, 193, 255, 321])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_matmul_rows_that_start_anywhere(torch, moe, N, dtype):
+    """Full and small tiles of groups whose output rows start on odd elements and end
+    inside every part of a segment."""
+    off = [2, 2, 160, 420, 423]
+    a, sa, w, sw = _operands(torch, moe, N, 430, N, 160, G=4)
+    for ld, shift in ((N, 0), (N + 1, 1), (N + 3, 0)):
+        buf = torch.full((430 * ld + shift,), 5.0, dtype=_dt(torch, dtype), device="cuda")
+        out = buf[shift:].view(430, ld)[:, :N]
+        out.fill_(77.0)
+        _check_matmul(torch, moe, a, sa, w, sw, off, dtype=dtype, out=out)
+        assert (buf[shift:].view(430, ld)[:, N:] == 5).all() and (buf[:shift] == 5).all()
+
+
 def test_matmul_scale_pitch_and_empty(torch, moe):
     a, sa, w, sw = _operands(torch, moe, 3, 20, 64, 272)
     wide = torch.full((3, 37), float("nan"), device="cuda")
