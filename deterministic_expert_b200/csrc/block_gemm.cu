@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       // any address) two slots ahead; the thread that copied a number multiplies
       // it.  A slot covers several blocks because every hand-over costs the
       // epilogue's warps about 100 cycles, and their round trip with the tensor
-      // core is what bounds full tiles (one block a slot: 94 us where this takes
-      // 76, M = 9472, N = 1024, K = 7168).
+      // core is what bounds full tiles (M = 9472, N = 1024, K = 7168: 71 us now; when
+      // four blocks a slot came in, it went from 94 to 76).
       const uint32_t sfull0 = mapa_u32(sfull, 0);
       const int i0 = threadIdx.x - 64;
       int slot = 0, fslot = 0;            // slot multiplied next, slot filled next
