@@ -184,12 +184,21 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
   }
 }
 
-// sigmoid(g) = 1 / (1 + 2^(-g log2 e)): the exponent's rounding is |g| 2^-24 of the
-// power's size, the two approximations an ulp or two.
-__device__ __forceinline__ float sigmoid_approx(float g) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));   // e infinite: 0
+// sigmoid(g) = 1 / (1 + e^-g), to 8 2^-24 relative for every g.  The power of 2 of
+// g log2 e rounded to fp32 would be |g| 2^-24 off; but a gate is a bf16 value, so its
+// product with a head of log2 e of 16 bits is exact, and the constant's tail goes into
+// the power as 1 - g tail (|g tail| < 4.4e-4 where e^-g is a number: its square's half
+// is below 10^-7).  A clamp is any fp32 value: there (ANY) what the product lost is
+// added to the tail.  ex2 4 2^-24, the correction, its product and 1 + e one each at
+// most, rcp 2.  Below -87.3 the result is 0.
+template <bool ANY>
+__device__ __forceinline__ float sigmoid_f32(float g) {
+  constexpr float kHead = 47274.f / 32768.f, kTail = 4.88849515e-6f;   // tail: 1 - head ln 2
+  const float t = g * -kHead;
+  float w = fmaf(g, -kTail, 1.f), p, r;
+  if (ANY) w = fmaf(fmaf(g, -kHead, -t), 0.693147181f, w);
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(p, w, 1.f)));   // p infinite: 0
   return r;
 }
 
@@ -203,7 +212,7 @@ template <int GLU, bool GRAD>
 __device__ __forceinline__ void glu_parts(float g, float u, const QuantArgs& a, float& av, float& bv, float& da,
                                           float& db) {
   if (GLU == kSitu) {
-    const float sg = sigmoid_approx(g);
+    const float sg = sigmoid_f32<false>(g);
     const float tg = tanhf(__fdiv_rn(g, a.beta_g)), tu = tanhf(__fdiv_rn(u, a.beta_u));
     av = a.beta_g * tg * sg;
     bv = a.beta_u * tu;
@@ -221,7 +230,7 @@ __device__ __forceinline__ void glu_parts(float g, float u, const QuantArgs& a, 
       db = (u > a.up_clamp || u < -a.up_clamp) ? 0.f : 1.f;
       bv = u > a.up_clamp ? a.up_clamp : (u < -a.up_clamp ? -a.up_clamp : u);
     }
-    const float sg = sigmoid_approx(g);
+    const float sg = sigmoid_f32<GLU == kSwigluClamped>(g);
     av = g * sg;
     if (GRAD) {
       da = sg * fmaf(g, 1.f - sg, 1.f);

@@ -625,7 +625,8 @@ typedef struct moe_glu_config {
 
 /* The gated unit h of rows [gate | up] (gu [rows, ld], 2 I columns used),
  * quantised from its fp32 value: codes [rows, I], scales [ceil(I / 128), ld_s].
- * I a multiple of 16; n_rows as above. */
+ * I a multiple of 16; n_rows as above.  The fp32 value is within 10 (SiTU-GLU: 24)
+ * times 2^-24 of h, relative, wherever sigmoid(gate) is at least 2^-126. */
 int moe_glu_quantize_fp8(const moe_glu_config* cfg, int rows, int I, const moe_bf16* gu, long long ld,
                          const int32_t* n_rows, uint8_t* codes, float* scales, long long ld_s, void* stream);
 

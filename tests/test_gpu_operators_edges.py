@@ -1,0 +1,73 @@
+"""The handle-free operators where a rounding in between would show: accuracy of the
+gated unit.
+
+U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
+within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
+division or product within U.
+"""
+import numpy as np
+import pytest
+
+import operators_ref as R
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def torch():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import deterministic_expert_b200
+    return deterministic_expert_b200
+
+
+# ------------------------------------------------------------- gated unit
+def _one_a_block(torch, values, width):
+    """bf16 rows [values, width], each block of 128 zero but for its first element."""
+    x = torch.zeros(len(values), width, dtype=torch.bfloat16)
+    x[:, ::128] = torch.tensor(values, dtype=torch.float32).to(torch.bfloat16)[:, None]
+    return x.cuda()
+
+
+def _values(scales):
+    """The magnitude of a block's only element: its scale is that / 448, rounded once."""
+    return scales.cpu().numpy().astype(np.float64) * 448.0
+
+
+def _bf16(torch, v):
+    return torch.tensor(v, dtype=torch.float32).to(torch.bfloat16).double().numpy()
+
+
+GATES = [float(v) for v in np.concatenate([np.linspace(-80, 80, 641), np.linspace(-3, 3, 97)])]
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(gate_clamp_max=90.0, up_clamp=2.0)], ids=str)
+def test_glu_is_accurate(torch, moe, kw):
+    """h = g sigmoid(g) to 10 U: the exponential 5 U, its sum with 1 U, the reciprocal
+    2 U, the product and the scale U each; the product with 1 is exact."""
+    g = _bf16(torch, GATES)
+    gu = torch.cat([_one_a_block(torch, GATES, 256), _one_a_block(torch, [1.0] * len(GATES), 256)], dim=1)
+    _, s = moe.glu_quantize_fp8(gu, **kw)
+    want = np.abs(g * R.sigmoid(g))
+    live = want > 0
+    for got in _values(s):
+        assert np.all(np.abs(got - want)[live] <= 10 * U * want[live])
+
+
+def test_glu_situ_is_accurate(torch, moe):
+    """h = bg tanh(g / bg) sigmoid(g) bu tanh(u / bu): two tanh of rounded arguments
+    10 U, the sigmoid 8 U, five products and the scale."""
+    g = _bf16(torch, GATES)
+    gu = torch.cat([_one_a_block(torch, GATES, 128), _one_a_block(torch, [1.0] * len(GATES), 128)], dim=1)
+    _, s = moe.glu_quantize_fp8(gu, activation=1, situ_beta_gate=1.5, situ_beta_up=2.0)
+    want = np.abs(1.5 * np.tanh(g / 1.5) * R.sigmoid(g) * 2 * np.tanh(0.5))
+    live = want > 0
+    assert np.all(np.abs(_values(s)[0] - want)[live] <= 24 * U * want[live])
