@@ -1,5 +1,5 @@
 """The handle-free operators where a rounding in between would show: accuracy of the
-gated unit.
+gated unit and its gradient.
 
 U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
 within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
@@ -71,3 +71,44 @@ def test_glu_situ_is_accurate(torch, moe):
     want = np.abs(1.5 * np.tanh(g / 1.5) * R.sigmoid(g) * 2 * np.tanh(0.5))
     live = want > 0
     assert np.all(np.abs(_values(s)[0] - want)[live] <= 24 * U * want[live])
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(gate_clamp_max=90.0, up_clamp=2.0)], ids=str)
+def test_glu_gradient_is_accurate(torch, moe, kw):
+    """da = s (1 + g (1 - s)) to 12 U of its terms s (1 + |g| (1 - s)): s 8 U, less the
+    more of it lies in 1 - s, which is as accurate; its product, the fused sum, the
+    product and the scale U each."""
+    g = _bf16(torch, GATES)
+    one = _one_a_block(torch, [1.0] * len(GATES), 128)
+    gu = torch.cat([_one_a_block(torch, GATES, 128), one], dim=1)
+    _, s = moe.glu_backward_quantize_fp8(gu, one, **kw)
+    sg, c = R.sigmoid(g), R.sigmoid(-g)
+    got, (up,) = _values(s[:1])[0], _values(s[1:])
+    live = np.abs(sg * (1 + g * c)) > 0
+    assert np.all(np.abs(got - np.abs(sg * (1 + g * c)))[live] <= 12 * U * (sg * (1 + np.abs(g) * c))[live])
+    h = np.abs(g * sg)
+    assert np.all(np.abs(up - h)[h > 0] <= 10 * U * h[h > 0])
+
+
+def test_glu_situ_gradient_is_accurate(torch, moe):
+    """The slope of a tanh is 1 - t^2, to 24 U of 1: t 5 U twice, its square and the
+    difference; the other factors as above."""
+    beta = 1.5
+    x = [v for v in GATES if abs(v) <= 30]
+    g = _bf16(torch, x)
+    one = _one_a_block(torch, [1.0] * len(x), 128)
+    edge = _one_a_block(torch, x, 128)
+    slope = 1 / np.cosh(g / beta) ** 2
+    # Of the up half: du = d a(g = 1) slope.
+    _, s = moe.glu_backward_quantize_fp8(torch.cat([one, edge], dim=1), one, activation=1, situ_beta_gate=beta, situ_beta_up=beta)
+    a1 = beta * np.tanh(1 / beta) * R.sigmoid(np.float64(1.0))
+    got = _values(s)[1]
+    got[got == 448] = 0      # a block of zeros has scale 1
+    assert np.all(np.abs(got - a1 * slope) <= 32 * U * a1)
+    # Of the gate half: dg = d b(u = 1) (slope sigmoid + a (1 - sigmoid)).
+    _, s = moe.glu_backward_quantize_fp8(torch.cat([edge, one], dim=1), one, activation=1, situ_beta_gate=beta, situ_beta_up=beta)
+    b = beta * np.tanh(1 / beta)
+    t2 = beta * np.tanh(g / beta) * R.sigmoid(g) * R.sigmoid(-g)
+    got = _values(s)[0]
+    got[got == 448] = 0
+    assert np.all(np.abs(got - np.abs(slope * R.sigmoid(g) + t2) * b) <= 40 * U * (R.sigmoid(g) + np.abs(t2)) * b)
