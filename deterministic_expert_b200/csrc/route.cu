@@ -9,12 +9,12 @@
 // (nxmr.cn "V4" article, §2.2; DeepSeek V4 infra notes, §6.3; the linux.do post on
 // MoE variants, "QuantileBalancing".)
 //
-// Selection follows the keys' order in exact arithmetic.  Without a bias the
-// scores grow with the logits, so the logits themselves are the keys and every
-// comparison is exact.  With one, keys are formed in fp32; where two neighbours in
-// the order lie within the error bound below, the slots' keys (and those of the
-// experts just left out) are formed again in fp64, one a lane; a row whose groups
-// are that close goes to a second pass that is fp64 throughout.
+// Without a bias the scores grow with the logits, so the logits themselves are the
+// keys and every comparison of two experts is exact.  With one, keys are formed in
+// fp32; where two neighbours in the order lie within the error bound below, the slots'
+// keys (and those of the experts just left out) are formed again in fp64, one a lane.
+// A row whose groups' fp32 sums are that close goes to a second pass in fp64, which
+// places groups without a bias by the logits (group_position).
 #include <cfloat>
 
 #include "common.cuh"
@@ -86,40 +86,72 @@ __device__ __forceinline__ float close_bound(float key, int softmax) {
   return fmaf(1.3e-7f, fabsf(key), softmax ? 1.1e-6f : 6.5e-7f);
 }
 
+// Where a group without a bias stands whose best logits are a >= b (-inf: it has only
+// one), as hi + lo that grows with the sum S of their scores and tells sums apart
+// where fp64 scores would all be 1 or 0:
+//   softmax  log S + const = a + log(1 + e^(b - a))
+//   sigmoid  S - 1 = sigmoid(a) - sigmoid(-b) = (1 - e^-(a + b)) sigmoid(a) sigmoid(b)
+//            between 1/2 and 3/2, log S below, -log(2 - S) above; 2 - S is the sum of
+//            (-b, -a), so that only sums below 1 have to be formed.
+__device__ __noinline__ double2 group_position(double a, double b, int softmax) {
+  const double ninf = -static_cast<double>(INFINITY);
+  auto sigmoid = [](double v) { return 1.0 / (1.0 + exp(-v)); };
+  double x = a, small;
+  bool low = true;
+  if (softmax) {
+    if (!(fabs(x) < -ninf)) return make_double2(x, 0.0);
+    small = log1p(exp(b - a));
+  } else {
+    const double s = b > ninf ? a + b : ninf;   // S < 1 exactly where a + b < 0
+    low = s < 0.0;
+    const double y = low ? b : -a;
+    if (!low) x = -b;
+    const double t = -expm1(-fabs(s)) * sigmoid(-x) * sigmoid(-y);   // 1 - S of (x, y)
+    if (t <= 0.5) return make_double2(low ? -t : t, 0.0);
+    if (!(fabs(x) < -ninf)) return make_double2(low ? x : -x, 0.0);
+    const double ex = exp(x);                   // S < 1/2, so x < 0
+    small = log1p(exp(y - x) * (1.0 + ex) / (1.0 + exp(y))) - log1p(ex);
+  }
+  const double hi = x + small, z = hi - x, lo = (x - (hi - z)) + (small - z);   // hi + lo = x + small
+  return low ? make_double2(hi, lo) : make_double2(-hi, -lo);
+}
+
 // The whole row again in fp64, for rows whose fp32 keys are too close to order.
+// Without a bias the logits stay the keys.
 // Returns the expert of slot `lane` (-1: none).
 template <int CPL, typename In>
 __device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, int lane, int first, int count) {
   const double ninf = -static_cast<double>(INFINITY);
   double key[CPL];
-  double m = ninf;
+  auto load = [&]() {
 #pragma unroll
-  for (int i = 0; i < CPL; ++i) {
-    key[i] = ninf;
-    if (i < count) {
-      const double l = static_cast<double>(to_float(row[first + i]));
-      if (l > ninf) { key[i] = l; m = fmax(m, l); }
+    for (int i = 0; i < CPL; ++i) {
+      const double l = i < count ? static_cast<double>(to_float(row[first + i])) : ninf;
+      key[i] = l > ninf ? l : ninf;
     }
-  }
-  if (a.softmax) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < CPL; ++i)
-      if (key[i] > ninf) { key[i] = exp(key[i] - m); sum += key[i]; }
-      else key[i] = ninf;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-#pragma unroll
-    for (int i = 0; i < CPL; ++i)
-      if (key[i] > ninf) key[i] /= sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < CPL; ++i)
-      if (key[i] > ninf) key[i] = 1.0 / (1.0 + exp(-key[i]));
-  }
+  };
+  load();
   if (a.bias != nullptr) {
+    if (a.softmax) {
+      double m = ninf, sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < CPL; ++i) m = fmax(m, key[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(kFull, m, o));
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+        if (key[i] > ninf) { key[i] = exp(key[i] - m); sum += key[i]; }
+        else key[i] = ninf;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+        if (key[i] > ninf) key[i] /= sum;
+    } else {
+#pragma unroll
+      for (int i = 0; i < CPL; ++i)
+        if (key[i] > ninf) key[i] = 1.0 / (1.0 + exp(-key[i]));
+    }
 #pragma unroll
     for (int i = 0; i < CPL; ++i)
       if (key[i] > ninf) {
@@ -140,13 +172,27 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, in
       m2 = fmax(lo, fmax(m2, o2));
       m1 = hi;
     }
-    // A group with one expert left scores by that one.
-    const double score = (a.group_top == 2 && m2 > ninf) ? m1 + m2 : m1;
+    // A group with one expert left scores by that one.  Positions that come out equal
+    // are ordered by the logits: b first, whose part in the sum is the smaller one.
+    double2 at = make_double2((a.group_top == 2 && m2 > ninf) ? m1 + m2 : m1, 0.0);
+    if (a.bias != nullptr) {
+      m1 = m2 = 0.0;
+    } else if (a.group_top == 2) {
+      if (m1 > ninf) at = group_position(m1, m2, a.softmax);
+      load();   // again: no register holds them over the call
+    }
     const int g = lane / a.lpg;
     int rank = 0;
     for (int q = 0; q < a.n_groups; ++q) {
-      const double sq = __shfl_sync(kFull, score, q * a.lpg);
-      if (sq > score || (sq == score && q < g)) ++rank;
+      const int from = q * a.lpg;
+      const double hq = __shfl_sync(kFull, at.x, from), lq = __shfl_sync(kFull, at.y, from);
+      const double bq = __shfl_sync(kFull, m2, from), aq = __shfl_sync(kFull, m1, from);
+      bool above = q < g;
+      if (aq != m1) above = aq > m1;
+      if (bq != m2) above = bq > m2;
+      if (lq != at.y) above = lq > at.y;
+      if (hq != at.x) above = hq > at.x;
+      rank += above ? 1 : 0;
     }
     if (rank >= a.topk_groups)
 #pragma unroll
@@ -184,8 +230,12 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, in
 // (1.3 us of memory) and takes 13.3 us, one token 4.3.  A lane's whole sort network
 // is cheaper than searching its keys in every round; a row that has to be decided
 // in fp64 costs the launch up to 8 us.
+// The resident CTAs keep the fp64 pass, which few rows take, from costing the others
+// registers (8 experts a lane: 70 without it, and 14.6 instead of 13.6 us for 8192 x
+// 256).  Two a lane would have to spill for more than four CTAs: 8192 x 64 takes 6.45
+// us with four, 6.84 with six.
 template <int CPL, typename In>
-__global__ void __launch_bounds__(256) k_route(const RouteOpArgs a) {
+__global__ void __launch_bounds__(256, CPL == 4 ? 5 : CPL <= 8 ? 4 : CPL <= 16 ? 2 : 1) k_route(const RouteOpArgs a) {
   griddep_wait();
   griddep_launch();
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;

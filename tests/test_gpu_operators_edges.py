@@ -1,10 +1,12 @@
 """The handle-free operators where a rounding in between would show: accuracy of the
-gated unit and its gradient.
+gated unit and its gradient, experts and groups whose scores saturate.
 
 U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
 within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
 division or product within U.
 """
+from decimal import Decimal, localcontext
+
 import numpy as np
 import pytest
 
@@ -112,3 +114,62 @@ def test_glu_situ_gradient_is_accurate(torch, moe):
     got = _values(s)[0]
     got[got == 448] = 0
     assert np.all(np.abs(got - np.abs(slope * R.sigmoid(g) + t2) * b) <= 40 * U * (R.sigmoid(g) + np.abs(t2)) * b)
+
+
+# ----------------------------------------------------------------- routing
+def _exact_route(l, k, scores, n_groups, keep):
+    """Experts of one row without a bias, groups scored by their two best, in decimals
+    long enough that nothing saturates."""
+    E = len(l)
+    n = E // n_groups
+    with localcontext() as ctx:
+        ctx.prec = 1200
+        ctx.Emin, ctx.Emax = -10 ** 9, 10 ** 9
+        d = [Decimal(float(v)) for v in l]
+        m = max(d)
+        f = (lambda v: 1 / (1 + (-v).exp())) if scores == "sigmoid" else (lambda v: (v - m).exp())
+        known = {}
+
+        def score(v):
+            if v not in known:
+                known[v] = f(v)
+            return known[v]
+
+        best = [sum(score(v) for v in sorted(d[g * n:(g + 1) * n], reverse=True)[:2]) for g in range(n_groups)]
+        # Within the context: a decimal's sign change rounds to it.
+        kept = sorted(range(n_groups), key=lambda g: (-best[g], g))[:keep]
+        inside = [e for e in range(E) if e // n in kept]
+        return sorted(inside, key=lambda e: (-d[e], e))[:k]
+
+
+def _saturated_rows(E, seed):
+    """Rows whose scores are 1 (or 0) to 64 bits, with distinct logits."""
+    rng = np.random.default_rng(seed)
+    f32 = np.float32
+    rows = [40 + np.arange(E) % 16, rng.uniform(38, 60, E), rng.uniform(28, 60, E), rng.uniform(28, 29, E),
+            50 + rng.permutation(E) * 3.8e-6, -60 - rng.uniform(0, 30, E), -800 - 3 * rng.permutation(E) % 400,
+            rng.uniform(-60, 60, E), np.where(np.arange(E) % 3 == 0, rng.uniform(40, 60, E), -rng.uniform(40, 60, E)),
+            rng.integers(28, 34, E)]
+    rows[1] = np.where(np.arange(E) == 5, 0.0, rows[1])          # softmax: the rest below exp(-745) of it
+    rows.append(np.where(np.arange(E) == 3, 1000.0, rng.integers(0, 40, E)))
+    rows.append(np.where(np.arange(E) % (E // 4) == 1, 900.0, rng.uniform(0, 60, E)))   # equal bests, the second decides
+    return np.array(rows, f32)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,keep,k", [(16, 4, 2, 2), (64, 8, 3, 6), (512, 4, 2, 8), (1024, 8, 4, 8)])
+def test_route_saturated_scores(torch, moe, scores, E, groups, keep, k):
+    l = _saturated_rows(E, E)
+    idx, _ = moe.route(torch.from_numpy(l).cuda(), k, scores=scores, n_groups=groups, topk_groups=keep, group_top=2,
+                       renormalize=True)
+    got = idx.cpu().numpy()
+    for t in range(len(l)):
+        assert got[t].tolist() == _exact_route(l[t], k, scores, groups, keep), (t, l[t][:16])
+
+
+def test_route_saturated_worked_examples(torch, moe):
+    kw = dict(scores="sigmoid", group_top=2)
+    idx, _ = moe.route(torch.arange(40.0, 56.0).cuda()[None], 2, n_groups=4, topk_groups=2, **kw)
+    assert idx.tolist() == [[15, 14]]
+    idx, _ = moe.route(torch.tensor([[40.0, 41, 39, 42, 40, 40, 38, 38]]).cuda(), 2, n_groups=2, topk_groups=1, **kw)
+    assert idx.tolist() == [[3, 1]]
