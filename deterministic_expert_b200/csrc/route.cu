@@ -78,12 +78,35 @@ __device__ __forceinline__ void sort_desc(uint32_t (&v)[N]) {
           }
 }
 
+// Sum of N values in pairs: log2 N roundings of each, not N - 1.
+template <int N, typename F>
+__device__ __forceinline__ float sum_in_pairs(F value) {
+  float part[6];   // part[b]: the sum of 2^b values
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float s = value(i);
+    int b = 0;
+#pragma unroll
+    for (; b < 6 && (i >> b & 1); ++b) s += part[b];
+    part[b] = s;
+  }
+  int top = 0;
+#pragma unroll
+  for (int b = 0; b < 6; ++b)
+    if (N >> b == 1) top = b;
+  return part[top];
+}
+
 // How far the difference of two fp32 keys of about this size can be from the exact
-// one.  sigmoid: below 3e-7 for s <= 1 (sigmoid_fast); softmax: the argument's
-// rounding, expf and the fp32 sum of up to 1024 terms, below 5e-7; the sum with the
-// bias 2^-24 |key|.  Each twice, for two keys.
+// one, u = 2^-24.  sigmoid: below 3e-7 each for s <= 1 (sigmoid_fast).  softmax, of
+// d = max - l: e^-d errs by |d| u (the argument) and 4 u (2 ulp), the reciprocal and
+// the product by 2 u, so p by (0.37 + 6 p) u; the sum by (ln E + 4) u and its at most
+// 5 + 5 additions (sum_in_pairs, warp_sum), an error that the two keys share: it counts
+// by p - p'.  As p + p' <= 1: 0.74 + 6 + 21 = 28 u.  The sum with the bias: u |key|
+// each.  (A bound that shrinks with the largest p spares softmax rows fp64 work but
+// costs the others a register: 13.65 -> 14.05 us for sigmoid rows of 256.)
 __device__ __forceinline__ float close_bound(float key, int softmax) {
-  return fmaf(1.3e-7f, fabsf(key), softmax ? 1.1e-6f : 6.5e-7f);
+  return fmaf(1.3e-7f, fabsf(key), softmax ? 1.7e-6f : 6.5e-7f);
 }
 
 // Where a group without a bias stands whose best logits are a >= b (-inf: it has only
@@ -273,11 +296,7 @@ __global__ void __launch_bounds__(256, CPL == 4 ? 5 : CPL <= 8 ? 4 : CPL <= 16 ?
 #pragma unroll
     for (int i = 0; i < CPL; ++i) rmax = fmaxf(rmax, l[i]);   // fmaxf drops a NaN
     rmax = warp_max(rmax);
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < CPL; ++i)
-      if (l[i] > -INFINITY) s += expf(l[i] - rmax);
-    rsum = warp_sum(s);
+    rsum = warp_sum(sum_in_pairs<CPL>([&](int i) { return l[i] > -INFINITY ? expf(l[i] - rmax) : 0.f; }));
   }
   auto score = [&](float v) { return a.softmax ? expf(v - rmax) / rsum : sigmoid_f32(v); };
 

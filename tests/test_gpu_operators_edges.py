@@ -1,5 +1,5 @@
 """The handle-free operators where a rounding in between would show: accuracy of the
-gated unit and its gradient, experts and groups whose scores saturate.
+gated unit and its gradient, experts and groups whose scores saturate or nearly tie.
 
 U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
 within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
@@ -173,3 +173,19 @@ def test_route_saturated_worked_examples(torch, moe):
     assert idx.tolist() == [[15, 14]]
     idx, _ = moe.route(torch.tensor([[40.0, 41, 39, 42, 40, 40, 38, 38]]).cuda(), 2, n_groups=2, topk_groups=1, **kw)
     assert idx.tolist() == [[3, 1]]
+
+
+@pytest.mark.parametrize("E", [64, 256, 512, 1024])
+def test_route_near_ties_beside_many_small_scores(torch, moe, E):
+    """One score of nearly 1 among many that an fp32 sum may drop one by one; a bias
+    lifts another key to within a few 1e-7 of the first."""
+    for base in (-16.645, -16.3, -16.9, -15.95, -17.4):
+        l = np.full((1, E), base, np.float32)
+        l[0, 0] = 0.0
+        s = R.scores_of(l[0].astype(np.float64), "softmax")[0]
+        for gap in (2e-7, 3e-7, 6e-7, 1e-6, -2e-7, -3e-7, -6e-7, -1e-6):
+            b = np.zeros(E, np.float32)
+            b[E // 2 + 3] = np.float32(s[0] - s[1] + gap)
+            idx, _ = moe.route(torch.from_numpy(l).cuda(), 1, bias=torch.from_numpy(b).cuda())
+            want, _ = R.route(l, 1, bias=b.astype(np.float64))
+            assert idx.cpu().numpy().tolist() == want.tolist(), (base, gap)
