@@ -341,11 +341,16 @@ __global__ void __launch_bounds__(256, CPL == 4 ? 5 : CPL <= 8 ? 4 : CPL <= 16 ?
       m1 = max(m1, o1);
     }
     uint32_t gscore = m1;
-    if (a.group_top == 2 && m1 != 0) {
+    // What the keys' and their sum's own roundings can be, 2 2^-24 of the keys' sizes:
+    // the sum may be far smaller than they are.  Infinite with them.
+    float slack = 0.f;
+    if (m1 != 0 && (a.bias != nullptr || a.group_top == 2)) {
       // Keys are logits without a bias; the sum is of their scores.
       const float v1 = a.bias != nullptr ? value_of(m1) : score(value_of(m1));
-      const float v2 = m2 == 0 ? 0.f : (a.bias != nullptr ? value_of(m2) : score(value_of(m2)));
+      float v2 = 0.f;
+      if (a.group_top == 2 && m2 != 0) v2 = a.bias != nullptr ? value_of(m2) : score(value_of(m2));
       gscore = order_of(v1 + v2);
+      slack = 1.3e-7f * (fabsf(v1) + fabsf(v2));
     }
     int rank = 0;
     for (int q = 0; q < a.n_groups; ++q) {
@@ -354,12 +359,15 @@ __global__ void __launch_bounds__(256, CPL == 4 ? 5 : CPL <= 8 ? 4 : CPL <= 16 ?
     }
     const bool stays = rank < a.topk_groups;
     if (a.bias != nullptr || a.group_top == 2) {
-      const uint32_t worst = __reduce_min_sync(kFull, g < a.n_groups && stays ? gscore : 0xffffffffu);
-      const uint32_t best = __reduce_max_sync(kFull, g < a.n_groups && !stays ? gscore : 0u);
-      if (best != 0 && worst != 0xffffffffu) {
-        const float vw = value_of(worst), vb = value_of(best);
-        close_groups = vw - vb <= 2.f * close_bound(vw, a.softmax);
-      }
+      // The lowest that a kept group may be, the highest that another may.
+      const float v = value_of(gscore);
+      const uint32_t low = slack < INFINITY ? order_of(v - slack) : order_of(-INFINITY);
+      const uint32_t high = slack < INFINITY ? order_of(v + slack) : order_of(INFINITY);
+      const bool has = g < a.n_groups && gscore != 0;
+      const uint32_t worst = __reduce_min_sync(kFull, has && stays ? low : 0xffffffffu);
+      const uint32_t best = __reduce_max_sync(kFull, has && !stays ? high : 0u);
+      if (best != 0 && worst != 0xffffffffu)
+        close_groups = !(value_of(worst) - value_of(best) > (a.softmax ? 1.8e-6f : 1.3e-6f));   // four scores' errors
     }
     if (!stays) {
 #pragma unroll

@@ -1,5 +1,6 @@
 """The handle-free operators where a rounding in between would show: accuracy of the
-gated unit and its gradient, experts and groups whose scores saturate or nearly tie.
+gated unit and its gradient, experts and groups whose keys saturate, cancel or
+nearly tie.
 
 U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
 within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
@@ -189,3 +190,27 @@ def test_route_near_ties_beside_many_small_scores(torch, moe, E):
             idx, _ = moe.route(torch.from_numpy(l).cuda(), 1, bias=torch.from_numpy(b).cuda())
             want, _ = R.route(l, 1, bias=b.astype(np.float64))
             assert idx.cpu().numpy().tolist() == want.tolist(), (base, gap)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", [100.0, 1000.0])
+def test_route_groups_whose_keys_cancel(torch, moe, scores, size):
+    """Biases that force one expert of a group on and another off: each key rounds at
+    its own size, their sum is small."""
+    rng = np.random.default_rng(int(size))
+    l = np.repeat(rng.uniform(-2, 2, (400, 1, 2)), 4, axis=1)
+    l = (l + rng.uniform(-2e-5, 2e-5, (400, 4, 2))).astype(np.float32).reshape(400, 8)
+    b = np.array([size, -size] * 4, np.float32)
+    kw = dict(scores=scores, n_groups=4, topk_groups=2, group_top=2, renormalize=True)
+    idx, _ = moe.route(torch.from_numpy(l).cuda(), 3, bias=torch.from_numpy(b).cuda(), **kw)
+    want, _ = R.route(l, 3, bias=b.astype(np.float64), **kw)
+    assert np.array_equal(idx.cpu().numpy(), want)
+
+
+def test_route_group_sums_past_fp32(torch, moe):
+    l = np.zeros((1, 8), np.float32)
+    b = np.array([3.0e38, 3.0e38, 3.2e38, 3.1e38, 3.3e38, 2.0e38, -3.3e38, -3.3e38], np.float32)
+    kw = dict(scores="sigmoid", n_groups=4, topk_groups=1, group_top=2)
+    idx, _ = moe.route(torch.from_numpy(l).cuda(), 2, bias=torch.from_numpy(b).cuda(), **kw)
+    want, _ = R.route(l, 2, bias=b.astype(np.float64), **kw)
+    assert want.tolist() == [[2, 3]] and idx.cpu().numpy().tolist() == want.tolist()
