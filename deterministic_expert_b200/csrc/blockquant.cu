@@ -30,6 +30,7 @@ constexpr float kE4m3Max = 448.f;
 // ulp, each product rounds by half of one: 2^-20 covers all of it four times).
 struct BlockScale {
   float s, inv, lo, hi;
+  float size, unit;   // 2^e and s / 2^e (2^e <= s)
   float rem;   // amax - 448 s, exact (0 for a raised scale, whose division is by a power of two)
 };
 
@@ -50,6 +51,9 @@ __device__ __forceinline__ BlockScale block_scale(float amax) {
     b.s = __int_as_float(0x7fffffff);
     b.inv = 0.f;
   }
+  const uint32_t e = __float_as_uint(b.s) & 0x7f800000u;
+  b.size = __uint_as_float(e);
+  b.unit = b.s * __uint_as_float(0x7f000000u - e);
   b.lo = b.inv * (1.f - 0x1p-20f);
   b.hi = b.inv * (1.f + 0x1p-20f);
   return b;
@@ -117,8 +121,11 @@ __device__ __forceinline__ uint2 codes8_bf16(const float (&v)[8], const BlockSca
     q[i] = mul2(x[i], f2);
   }
   if (b.rem == 0.f) {
-    // q - (q s - x) f: with a zero remainder (always +0) a zero keeps its sign.
-    const uint64_t s2 = pair(b.s, b.s), one = pair(-1.f, -1.f), n2 = pair(-f, -f);
+    // q - (q s - x) f: with a zero remainder (always +0) a zero keeps its sign.  The
+    // remainder is about x 2^-24, which would underflow for small s, so that it is
+    // formed of x and s divided by 2^e.
+    const float up = __uint_as_float(0x7f000000u - __float_as_uint(b.size)), down = f * b.size;
+    const uint64_t s2 = pair(b.unit, b.unit), one = pair(-up, -up), n2 = pair(-down, -down);
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = fma2(fma2(q[i], s2, mul2(x[i], one)), n2, q[i]);
   }
@@ -256,15 +263,15 @@ __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantA
 // threads takes 32 rows (their scales of a block are one 128-byte segment) and
 // walks their blocks, U at a time so that their loads are in flight together.
 // Bound by memory: every element is read once and its code written once.  24576 bf16
-// rows of 2048: 25.4 us (6.0 TB/s; two blocks at a time 27.3), and 24.7 us gathered
-// from 4096 rows, which then come through L2.  Gated unit of 32768 x 2048: 61 us
+// rows of 2048: 26.2 us (5.8 TB/s; with three resident CTAs, where the compiler would
+// take 67 registers, 27.8), and 22.7 us a call gathered from 4096 rows, which then come through L2.  Gated unit of 32768 x 2048: 61 us
 // (5.5 TB/s); its gradient, 24576 x 1408: 55 us (5.0 TB/s).
 constexpr int kRowsPerCta = 32;
 template <int KIND>
 constexpr int kUnroll = KIND == kQuantBf16 ? 4 : 1;
 
 template <int KIND, int GLU = kSwiglu>
-__global__ void __launch_bounds__(256) k_quant_blocks(const QuantArgs a) {
+__global__ void __launch_bounds__(256, KIND == kQuantBf16 ? 4 : 1) k_quant_blocks(const QuantArgs a) {
   constexpr int U = kUnroll<KIND>;
   constexpr bool GRAD = KIND == kQuantGluBackward;
   griddep_wait();

@@ -1,6 +1,6 @@
-"""The handle-free operators where a rounding in between would show: accuracy of the
+"""The handle-free operators where fp32 alone would decide wrongly: accuracy of the
 gated unit and its gradient, experts and groups whose keys saturate, cancel or
-nearly tie.
+nearly tie, blocks of tiny values.
 
 U = 2^-24 is half a step of fp32 relative to the value; an approximate power of 2 is
 within 4 U, an approximate reciprocal within 2 U, tanhf within 2 ulp (4 U), a sum,
@@ -214,3 +214,48 @@ def test_route_group_sums_past_fp32(torch, moe):
     idx, _ = moe.route(torch.from_numpy(l).cuda(), 2, bias=torch.from_numpy(b).cuda(), **kw)
     want, _ = R.route(l, 2, bias=b.astype(np.float64), **kw)
     assert want.tolist() == [[2, 3]] and idx.cpu().numpy().tolist() == want.tolist()
+
+
+# ------------------------------------------------------------ quantisation
+def _tiny_blocks(exact_in):
+    """Blocks whose scale is exact (or raised to 2^-126), filled with exact middles of
+    codes and their neighbours, the maxima from 2^-133 to 2^-105."""
+    mids = (R.GRID[1:] + R.GRID[:-1]) / 2
+    rows = []
+    for k in range(-143, -112):
+        for c in range(16, 32):
+            s = max(c * 2.0 ** k, 2.0 ** -126)
+            amax = 448.0 * c * 2.0 ** k
+            x = np.concatenate([mids, R.GRID[:-1]]) * s
+            x = x[(x <= amax) & exact_in(x)]
+            if not exact_in(np.array([amax]))[0]:
+                continue
+            x = np.resize(np.concatenate([[amax], x]), 128) * np.resize([1.0, -1.0, 1.0], 128)
+            x[0] = amax
+            rows.append(x)
+    return np.array(rows)
+
+
+def test_quantize_tiny_blocks_fp32(torch, moe):
+    x = _tiny_blocks(lambda v: v.astype(np.float32).astype(np.float64) == v)
+    q, s = moe.quantize_rows_fp8(torch.from_numpy(x.astype(np.float32)).cuda())
+    rq, rs = R.quantize_rows(x)
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+
+
+def _bf16_exact(v):
+    f = v.astype(np.float32)
+    return (f.astype(np.float64) == v) & ((f.view(np.uint32) & 0xFFFF) == 0)
+
+
+def test_quantize_tiny_blocks_bf16(torch, moe):
+    x = _tiny_blocks(_bf16_exact)
+    bits = (x.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16)
+    xt = torch.from_numpy(bits.view(np.int16)).cuda().view(torch.bfloat16)
+    q, s = moe.quantize_rows_fp8(xt)
+    rq, rs = R.quantize_rows(x)
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+    # The weights' quantiser: the same blocks, one above the other.
+    for r in range(0, len(x), 37):
+        w, ws = moe.quantize_weights_fp8(xt[r:r + 1])
+        assert np.array_equal(w.cpu().numpy(), rq[r:r + 1]) and float(ws[0, 0]) == float(rs[0, r])
