@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
     }
     mbar_init(&bars[kDoneBar], 1);
     for (int i = 0; i < kScaleSlots; ++i) {
-      mbar_init(&bars[kDoneBar + 1 + i], 4);   // both CTAs' scale warps
+      mbar_init(&bars[kDoneBar + 1 + i], 2);   // this CTA's scale warps
       mbar_init(&bars[kDoneBar + 1 + kScaleSlots + i], kEpiW);
     }
     abort_flag = 0;
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       // The whole warp walks the loop (its addresses stay in uniform registers); one
       // lane issues.
       const bool issuer = elect_one();
-      int stage = 0, buf = 0, slot = 0;
-      uint32_t phase = 0, bphase = 0, sphase = 0;
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, bphase = 0;
       // Low words of the operands' descriptors: start address and leading offset, >> 4.
       const uint32_t tok_lo = (((smem0 + S * kWSlot) >> 4) & 0x3FFFu) | 1u << 16;
       const uint32_t w_lo = ((smem0 >> 4) & 0x3FFFu) | (TRANS ? 16384u >> 4 : 1u) << 16;
@@ -483,12 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         uint32_t d = 0;
         for (int kb = 0; kb < nkb; ++kb) {
           ok = bar_wait(full + 8 * stage, phase, abort);
-          if (kb % kSlotBlocks == 0) {
-            // The scales of these blocks are there before their products are begun, so
-            // the epilogue, which waits for the products, need not wait for them too.
-            ok = ok && bar_wait(sfull + 8 * slot, sphase, abort);
-            if (++slot == kScaleSlots) { slot = 0; sphase ^= 1u; }
-          }
           if (left == 0) {
             ok = ok && bar_wait(tempty + 8 * buf, bphase ^ 1u, abort);
             left = ti.batch;
@@ -534,7 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       // epilogue's warps about 100 cycles, and their round trip with the tensor
       // core is what bounds full tiles (M = 9472, N = 1024, K = 7168: 71 us now; when
       // four blocks a slot came in, it went from 94 to 76).
-      const uint32_t sfull0 = mapa_u32(sfull, 0);
       const int i0 = threadIdx.x - 64;
       int slot = 0, fslot = 0;            // slot multiplied next, slot filled next
       uint32_t fphase = 0;
@@ -598,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(sfull0 + 8 * slot);
+          if (lane == 0) bar_arrive(sfull + 8 * slot);
           if (++slot == kScaleSlots) slot = 0;
         }
       }
@@ -611,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t tempty0 = mapa_u32(tempty, 0);
     const uint32_t tlane = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    int buf = 0, slot = 0;
+    int buf = 0, slots = 0;   // slots read: slot and parity in one
     uint32_t bphase = 0;
     bool ok = true;
     for (int t = pair; ok && t < total; t += pairs) {
@@ -619,8 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      auto wait_products = [&]() {
+      // Products, and before the first read of a slot its scales: those are there long
+      // before, so both are tried at once.
+      auto wait_products = [&](bool scales_too) {
+        const uint32_t sbar = sfull + 8 * (slots % kScaleSlots), sparity = slots / kScaleSlots & 1;
+        bool there = true;
+        if (scales_too) there = bar_try(sbar, sparity);
         ok = bar_wait(tfull + 8 * buf, bphase, abort);
+        if (!there) ok = ok && bar_wait(sbar, sparity, abort);
         ok = __all_sync(kFull, ok);
         tc_fence_after();
         return ok;
@@ -633,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
       };
       auto give_scales = [&]() {
         __syncwarp();
-        if (lane == 0) bar_arrive(sempty + 8 * slot);
-        if (++slot == kScaleSlots) slot = 0;
+        if (lane == 0) bar_arrive(sempty + 8 * (slots % kScaleSlots));
+        slots = (slots + 1) % (2 * kScaleSlots);
       };
       // Full tiles: one block a buffer, four chunks of 32 columns, each one's load under
       // the multiply-adds of the one before, across blocks too: the next block's first
@@ -648,12 +647,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
 #pragma unroll
           for (int i = 0; i < 16; ++i) fma2(acc[c * 16 + i], pack2u(x[2 * i], x[2 * i + 1]), s2);
         };
-        if (!wait_products()) return;
+        if (!wait_products(true)) return;
         tmem_ld32(tlane + buf * 256 + half * 128, v[0]);
         for (int kb = 0; kb < nkb; ++kb) {
           const int z = kb % kSlotBlocks;
           const uint32_t tb = tlane + buf * 256 + half * 128;
-          if (z == 0) s4 = ld_shared_f32x4(scales + slot * kSlotBytes + (half * 128 + q * 32 + lane) * 16);
+          if (z == 0) {
+            s4 = ld_shared_f32x4(scales + slots % kScaleSlots * kSlotBytes + (half * 128 + q * 32 + lane) * 16);
+            give_scales();
+          }
           const uint64_t s2 = pack2(s4.x, s4.x);
           tmem_wait32(v[0]);
           tmem_ld32(tb + 32, v[1]);
@@ -667,12 +669,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
           tmem_wait32(v[1]);
           release();
           if (kb + 1 < nkb) {
-            if (!wait_products()) return;
+            if (!wait_products(z == kSlotBlocks - 1)) return;
             tmem_ld32(tlane + buf * 256 + half * 128, v[0]);
           }
           add(3, v[1], s2);
           s4 = make_float4(s4.y, s4.z, s4.w, 0.f);
-          if (z == kSlotBlocks - 1 || kb == nkb - 1) give_scales();
         }
       };
       // Swapped tiles: BATCH blocks a buffer; the 128 / BATCH columns that a warp can
@@ -681,9 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         constexpr int BATCH = decltype(batch)::value, CH = decltype(chunk)::value, N = 128 / BATCH / CH;
         for (int kb = 0; kb < nkb; kb += BATCH) {
           const int z = kb % kSlotBlocks;
-          if (!wait_products()) return;
+          if (!wait_products(z == 0)) return;
           const uint32_t tb = tlane + buf * 256 + half * hc;
-          const uint32_t sc = scales + slot * kSlotBytes + (z * 256 + half * hc) * 4;
+          const uint32_t sc = scales + slots % kScaleSlots * kSlotBytes + (z * 256 + half * hc) * 4;
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             if (c * CH >= hc) break;
