@@ -971,7 +971,7 @@ class EPMoELayer:
 # surface; they are loaded on first use, as they need torch to be imported.
 OPERATORS = ("route", "route_backward", "group_rows", "quantize_rows_fp8", "quantize_weights_fp8",
              "glu_quantize_fp8", "glu_backward_quantize_fp8", "matmul_fp8", "combine_rows",
-             "combine_rows_backward", "operator_error")
+             "combine_rows_backward", "operator_error", "selftest_matmul_timeout")
 
 
 def __getattr__(name):

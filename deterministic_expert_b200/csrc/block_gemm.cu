@@ -293,13 +293,12 @@ __device__ __forceinline__ void ld_shared_pairs(uint32_t p, uint64_t& lo, uint64
 }
 
 // A bounded wait: every failed try sleeps in hardware for up to about a
-// microsecond, so the limit is of the order of seconds.  On time-out it raises the
-// CTA's abort flag and the device's error word; it gives up at once when another
-// role has.
-constexpr int kTries = 4 << 20;
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort) {
+// microsecond, so the limit (BlockGemmArgs::tries) is of the order of seconds.  On
+// time-out it raises the CTA's abort flag and the device's error word; it gives up at
+// once when another role has.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint32_t abort, int tries) {
   if (bar_try(bar, parity)) return true;
-  for (int i = 0; i < kTries; ++i) {
+  for (int i = 0; i < tries; ++i) {
     if (bar_try(bar, parity)) return true;
     if (ld_shared_i32(abort) != 0) return false;
   }
@@ -445,8 +444,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
           ok = false;
           break;
         }
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!bar_wait(empty + 8 * stage, phase ^ 1u, abort)) { ok = false; break; }
+        for (int kb = 0; kb < a.load_blocks; ++kb) {
+          if (!bar_wait(empty + 8 * stage, phase ^ 1u, abort, a.tries)) { ok = false; break; }
           // The even CTA counts both CTAs' bytes.
           if (leader)
             asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * stage),
@@ -459,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
           issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
           if (++stage == S) { stage = 0; phase ^= 1u; }
         }
+        if (a.load_blocks < nkb) ok = false;   // the self-test's
       }
       if (!ok && leader)
         for (int s = 0; s < S; ++s)
@@ -482,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         int left = 0;   // blocks that the current buffer still takes
         uint32_t d = 0;
         for (int kb = 0; kb < nkb; ++kb) {
-          ok = bar_wait(full + 8 * stage, phase, abort);
+          ok = bar_wait(full + 8 * stage, phase, abort, a.tries);
           if (left == 0) {
-            ok = ok && bar_wait(tempty + 8 * buf, bphase ^ 1u, abort);
+            ok = ok && bar_wait(tempty + 8 * buf, bphase ^ 1u, abort, a.tries);
             left = ti.batch;
             d = tmem_base + buf * 256;
           }
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         };
         auto fill = [&](int j) {
           if (j < nsl) {
-            ok = ok && bar_wait(sempty + 8 * fslot, fphase ^ 1u, abort);
+            ok = ok && bar_wait(sempty + 8 * fslot, fphase ^ 1u, abort, a.tries);
             for (int z = 0; ok && z < kSlotBlocks && j * kSlotBlocks + z < nkb; ++z) {
               const float* p = ps + static_cast<long long>(j * kSlotBlocks + z) * a.ld_as;
 #pragma unroll
@@ -618,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_block_gemm(const __grid_constan
         const uint32_t sbar = sfull + 8 * (slots % kScaleSlots), sparity = slots / kScaleSlots & 1;
         bool there = true;
         if (scales_too) there = bar_try(sbar, sparity);
-        ok = bar_wait(tfull + 8 * buf, bphase, abort);
-        if (!there) ok = ok && bar_wait(sbar, sparity, abort);
+        ok = bar_wait(tfull + 8 * buf, bphase, abort, a.tries);
+        if (!there) ok = ok && bar_wait(sbar, sparity, abort, a.tries);
         ok = __all_sync(kFull, ok);
         tc_fence_after();
         return ok;
@@ -847,8 +847,8 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
 }
 // bar_wait for a barrier that another CTA of the cluster arrives on after writing
 // this CTA's shared memory.
-__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t abort) {
-  for (int i = 0; i < kTries; ++i) {
+__device__ __forceinline__ bool bar_wait_cluster(uint32_t bar, uint32_t parity, uint32_t abort, int tries) {
+  for (int i = 0; i < tries; ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
@@ -925,10 +925,10 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_block_gemm_thin(const __gri
       }
       int last[kThinMost];   // parity of the copy last issued to a stage
       for (int s = 0; s < S; ++s) last[s] = -1;
-      for (int i = 0; ok && i < n; ++i) {
+      for (int i = 0; ok && i < min(n, a.load_blocks); ++i) {
         const int s = i % S;
         const uint32_t ph = static_cast<uint32_t>(i / S) & 1u;
-        if (!bar_wait(empty + 8 * s, ph ^ 1u, abort)) { ok = false; break; }
+        if (!bar_wait(empty + 8 * s, ph ^ 1u, abort, a.tries)) { ok = false; break; }
         asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * s),
                      "r"(bytes + kWSlot) : "memory");
         tma_load_2d(sA + s * a.a_slot, &a.mapA[box], (kb0 + i) * 128, ti.row0,
@@ -937,7 +937,7 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_block_gemm_thin(const __gri
         else tma_load_3d(sW + s * kWSlot, &a.mapW, (kb0 + i) * 128, ti.n0, ti.g, full + 8 * s);
         last[s] = static_cast<int>(ph);
       }
-      if (!ok)
+      if (!ok || a.load_blocks < n)
         for (int s = 0; s < S; ++s)
           if (last[s] >= 0) mbar_wait_drain(reinterpret_cast<uint64_t*>(smem + kThinRing) + s, last[s], kDrain);
     } else if (warp == 1) {
@@ -949,7 +949,7 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_block_gemm_thin(const __gri
       int s = 0;
       uint32_t ph = 0;
       for (int i = 0; i < n; ++i) {
-        const bool ok = bar_wait(full + 8 * s, ph, abort);
+        const bool ok = bar_wait(full + 8 * s, ph, abort, a.tries);
         if (!__all_sync(kFull, ok)) break;
         tc_fence_after();
         const uint32_t alo = w_lo + s * (kWSlot >> 4), blo = tok_lo + s * (static_cast<uint32_t>(a.a_slot) >> 4);
@@ -980,8 +980,8 @@ __global__ void __launch_bounds__(kThinThreads, 1) k_block_gemm_thin(const __gri
     } else if (warp >= 4) {
       const int q = warp & 3, row = q * 32 + lane;   // TMEM lane = weight row
       const uint32_t tl = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-      bool ok = bar_wait(sfull, 0, abort) && bar_wait(tfull, 0, abort);
-      if (rank > 0) ok = ok && bar_wait_cluster(sums_in, 0, abort);
+      bool ok = bar_wait(sfull, 0, abort, a.tries) && bar_wait(tfull, 0, abort, a.tries);
+      if (rank > 0) ok = ok && bar_wait_cluster(sums_in, 0, abort, a.tries);
       ok = __all_sync(kFull, ok);
       tc_fence_after();
       const int col = ti.n0 + row;

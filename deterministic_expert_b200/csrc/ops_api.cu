@@ -234,9 +234,14 @@ int moe_glu_backward_quantize_fp8(const moe_glu_config* cfg, int rows, int I, co
   return status(launch_quant_blocks(a, kQuantGluBackward, static_cast<cudaStream_t>(stream)));
 }
 
-int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, int K, const uint8_t* a,
-                   const float* a_scale, long long ld_as, const uint8_t* w, const float* w_scale, void* out,
-                   int out_dtype, long long ldo, void* stream) {
+// Tries of a bounded wait, of up to about a microsecond each.
+constexpr int kTries = 4 << 20;
+
+// load_blocks: blocks of the contraction that are loaded, below all of them only in
+// the waits' self-test.
+static int matmul(int transposed, int G, const int32_t* offsets, int M, int N, int K, const uint8_t* a,
+                  const float* a_scale, long long ld_as, const uint8_t* w, const float* w_scale, void* out,
+                  int out_dtype, long long ldo, int load_blocks, int tries, void* stream) {
   if (G <= 0 || M < 0 || N <= 0 || K <= 0 || !dtype_ok(out_dtype) || (transposed != 0 && transposed != 1) ||
       (G > 1 && M > 0 && !offsets))
     return MOE_EINVAL;
@@ -306,9 +311,40 @@ int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, 
   g.ldo = ldo;
   g.out_f32 = out_dtype == MOE_DTYPE_F32;
   g.out_vec = al(out, 16) && pitch16(ldo, osize);
+  g.load_blocks = static_cast<int>(std::min<long long>(nkb, load_blocks));
+  g.tries = tries;
   const long long max_tiles = split ? thin_tiles : std::min<long long>(ntn * ((M + tr - 1) / tr + G), pairs);
   return status(launch_block_gemm(g, static_cast<int>(max_tiles),
                                   static_cast<cudaStream_t>(stream)));
+}
+
+int moe_matmul_fp8(int transposed, int G, const int32_t* offsets, int M, int N, int K, const uint8_t* a,
+                   const float* a_scale, long long ld_as, const uint8_t* w, const float* w_scale, void* out,
+                   int out_dtype, long long ldo, void* stream) {
+  return matmul(transposed, G, offsets, M, N, K, a, a_scale, ld_as, w, w_scale, out, out_dtype, ldo, INT_MAX, kTries,
+                stream);
+}
+
+int moe_selftest_matmul_timeout(int M, int N, int K, int load_blocks, void* stream) {
+  if (M < 1 || M > 8192 || N < 1 || N > 8192 || K < 1 || K > 8192 || load_blocks < 0) return MOE_EINVAL;
+  if (K % 16) return MOE_EUNSUPPORTED;
+  // Rows, weights, their scales, the product: all zeros.
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t kb = (K + 127) / 128, nb = (N + 127) / 128;
+  const size_t sizes[5] = {up(size_t(M) * K), up(size_t(N) * K), up(kb * M * 4), up(nb * kb * 4), up(size_t(M) * N * 4)};
+  size_t at[6] = {};
+  for (int i = 0; i < 5; ++i) at[i + 1] = at[i] + sizes[i];
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* p = nullptr;
+  if (cudaMalloc(&p, at[5]) != cudaSuccess) return status(cudaErrorMemoryAllocation);
+  int res = status(cudaMemsetAsync(p, 0, at[5], s));
+  if (res == MOE_OK)
+    res = matmul(0, 1, nullptr, M, N, K, p, reinterpret_cast<float*>(p + at[2]), M, p + at[1],
+                 reinterpret_cast<float*>(p + at[3]), p + at[4], MOE_DTYPE_F32, N, load_blocks, 1 << 14, s);
+  if (res == MOE_OK) res = moe_get_operator_error(s);   // synchronises
+  cudaStreamSynchronize(s);
+  cudaFree(p);
+  return res;
 }
 
 int moe_combine_rows(int T, int k, int D, int rows, const void* y, int y_dtype, long long ld_y,

@@ -96,6 +96,8 @@ struct BlockGemmArgs {
   long long ldo;
   int out_f32;
   int out_vec;            // rows of out start on 16-byte boundaries
+  int load_blocks;        // blocks of the contraction that are loaded: all (fewer: the waits' self-test)
+  int tries;              // limit of a wait
 };
 cudaError_t launch_block_gemm(const BlockGemmArgs& a, int max_tiles, cudaStream_t s);
 int block_gemm_pairs();                       // CTA pairs resident at once (0: the device cannot run it)

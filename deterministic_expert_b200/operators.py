@@ -47,6 +47,7 @@ ARGTYPES = {
     "moe_combine_rows": [_i, _i, _i, _i, _vp, _i, _ll, _vp, _vp, _vp, _vp, _i, _vp],
     "moe_combine_rows_backward": [_i, _i, _i, _i, _vp, _vp, _i, _ll, _vp, _vp, _vp, _vp, _vp],
     "moe_get_operator_error": [_vp],
+    "moe_selftest_matmul_timeout": [_i, _i, _i, _i, _vp],
 }
 _fns: dict = {}
 _Tensor = torch.Tensor
@@ -407,3 +408,10 @@ def operator_error(device=None, stream=None) -> int:
     with torch.cuda.device(dev):
         s = _raw_stream(torch.cuda.current_device()) if stream is None else _handle(stream)
         return int(_fn("moe_get_operator_error")(s))
+
+
+def selftest_matmul_timeout(M: int, N: int, K: int, load_blocks: int, stream=None) -> int:
+    """moe_selftest_matmul_timeout on the current device: the status after a product
+    whose loads stop early (MOE_ETIMEOUT: its bounded waits ran out)."""
+    s = _raw_stream(torch.cuda.current_device()) if stream is None else _handle(stream)
+    return int(_fn("moe_selftest_matmul_timeout")(M, N, K, load_blocks, s))

@@ -682,6 +682,14 @@ int moe_combine_rows_backward(int T, int k, int D, int rows, const moe_bf16* dou
  * Synchronises `stream`; not to be called while it is being captured. */
 int moe_get_operator_error(void* stream);
 
+/* Self-test of the bounded waits of moe_matmul_fp8: a product of zeros (M, N, K up to
+ * 8192, K a multiple of 16) whose loads stop after `load_blocks` blocks of each tile's
+ * contraction (of each CTA's share where few rows divide it), so that the waits for the
+ * others run out, after some 10 ms instead of seconds.  Returns MOE_ETIMEOUT, MOE_OK
+ * where nothing was left to wait for; the error word is clear afterwards, the context
+ * usable.  Allocates and frees; synchronises `stream`. */
+int moe_selftest_matmul_timeout(int M, int N, int K, int load_blocks, void* stream);
+
 int moe_destroy(moe_handle* h);
 const char* moe_status_string(int status);
 

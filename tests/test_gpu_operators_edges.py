@@ -259,3 +259,32 @@ def test_quantize_tiny_blocks_bf16(torch, moe):
     for r in range(0, len(x), 37):
         w, ws = moe.quantize_weights_fp8(xt[r:r + 1])
         assert np.array_equal(w.cpu().numpy(), rq[r:r + 1]) and float(ws[0, 0]) == float(rs[0, r])
+
+
+# ---------------------------------------------------------------- time-outs
+@pytest.mark.parametrize("M,N,K,loaded", [(8, 128, 4096, 0), (8, 128, 4096, 3), (20, 300, 8192, 1), (100, 512, 2048, 6),
+                                          (600, 512, 8192, 0), (2560, 2048, 2048, 0), (2560, 2048, 2048, 9),
+                                          (2560, 2048, 8192, 20)])
+def test_matmul_waits_run_out(torch, moe, M, N, K, loaded):
+    """Loads that stop early (clusters that divide a contraction, small tiles, full
+    ones): the error word says so once, the next products are right."""
+    from deterministic_expert_b200 import selftest_matmul_timeout
+    g = torch.Generator().manual_seed(M)
+    a, sa = moe.quantize_rows_fp8(torch.randn(700, 1024, generator=g).cuda())
+    w, sw = moe.quantize_weights_fp8(torch.randn(384, 1024, generator=g).to(torch.bfloat16).cuda())
+    parts = [slice(0, 8), slice(8, 90), slice(0, 700)]
+    want = [moe.matmul_fp8(a[p], sa[:, p], w, sw) for p in parts]
+    assert moe.operator_error() == moe.MOE_OK
+    assert selftest_matmul_timeout(M, N, K, loaded) == moe.MOE_ETIMEOUT
+    assert moe.operator_error() == moe.MOE_OK
+    for _ in range(3):
+        for p, x in zip(parts, want):
+            assert torch.equal(moe.matmul_fp8(a[p], sa[:, p], w, sw), x)
+    assert moe.operator_error() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 128, 1024), (300, 512, 1024), (2560, 2048, 1024)])
+def test_matmul_waits_do_not_run_out_otherwise(torch, moe, M, N, K):
+    from deterministic_expert_b200 import selftest_matmul_timeout
+    assert selftest_matmul_timeout(M, N, K, K // 128) == moe.MOE_OK
+    assert selftest_matmul_timeout(M, N, K, 1000) == moe.MOE_OK

@@ -165,6 +165,13 @@ def test_combine_refuses():
     assert b(4, 2, 64, 8, FAKE, FAKE, 0, 64, FAKE, None, None, FAKE, None) == moe.MOE_EINVAL
 
 
+def test_matmul_self_test_refuses():
+    f = ops._fn("moe_selftest_matmul_timeout")
+    for args in ((0, 128, 128, 1), (9000, 128, 128, 1), (8, 0, 128, 1), (8, 128, 0, 1), (8, 128, 9000, 1), (8, 128, 128, -1)):
+        assert f(*args, None) == moe.MOE_EINVAL, args
+    assert f(8, 128, 120, 1, None) == moe.MOE_EUNSUPPORTED
+
+
 def test_binding_refuses_host_tensors():
     x = torch.zeros(4, 128, dtype=torch.bfloat16)
     i = torch.zeros(4, 2, dtype=torch.int32)
