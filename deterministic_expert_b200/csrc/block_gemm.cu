@@ -70,8 +70,13 @@ constexpr int kSmem = 1024 + kRing + kBarSpace + kEpiW * kEpiSlot + kScaleSlots 
 static_assert(kRing / (kWSlot + 16 * 128) <= kRingMost, "stages");
 static_assert(kSlotBlocks == 4, "the epilogue reads a row's scales of a slot as one float4");
 
-// Error word of the handle-free operators on this device.
+// Error word of the handle-free operators on this device, and what was last taken from
+// it (under a lock on the host).
 __device__ int g_operator_error;
+__device__ int g_operator_taken;
+
+// One exchange: an error that another stream raises meanwhile is in it or stays.
+__global__ void k_take_operator_error() { g_operator_taken = atomicExch(&g_operator_error, 0); }
 
 struct BTile {
   int g, row0, rows, n0, nt;   // group, first row, valid rows, first output column, N of the MMA
@@ -1132,10 +1137,14 @@ cudaError_t launch_block_gemm(const BlockGemmArgs& a, int max_tiles, cudaStream_
 }
 
 cudaError_t read_operator_error(int* value, cudaStream_t s) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
   void* p = nullptr;
-  cudaError_t rc = cudaGetSymbolAddress(&p, g_operator_error);
+  cudaError_t rc = cudaGetSymbolAddress(&p, g_operator_taken);
+  if (rc != cudaSuccess) return rc;
+  k_take_operator_error<<<1, 1, 0, s>>>();
+  rc = cudaGetLastError();
   if (rc == cudaSuccess) rc = cudaMemcpyAsync(value, p, sizeof(int), cudaMemcpyDeviceToHost, s);
-  if (rc == cudaSuccess) rc = cudaMemsetAsync(p, 0, sizeof(int), s);
   if (rc == cudaSuccess) rc = cudaStreamSynchronize(s);
   return rc;
 }

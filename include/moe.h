@@ -676,10 +676,13 @@ int moe_combine_rows_backward(int T, int k, int D, int rows, const moe_bf16* dou
                               long long ld_y, const int32_t* row_of_slot, const float* w, void* dy, float* dw,
                               void* stream);
 
-/* Read and clear the current device's error word of moe_matmul_fp8: MOE_OK;
- * MOE_ETIMEOUT when a bounded device wait gave up (its output is incomplete);
- * MOE_ECUDA when the copy failed or the word holds a value no kernel writes.
- * Synchronises `stream`; not to be called while it is being captured. */
+/* Read and clear, in one exchange, the current device's error word of
+ * moe_matmul_fp8: MOE_OK; MOE_ETIMEOUT when a bounded device wait gave up (its
+ * output is incomplete); MOE_EINDEX when a kernel found a tile larger than the
+ * buffers that the host sized (its output is incomplete); MOE_ECUDA when the read
+ * failed or the word holds a value no kernel writes.  The word is the device's:
+ * an error of a product on any stream that ran before.  Synchronises `stream`; not to
+ * be called while it is being captured. */
 int moe_get_operator_error(void* stream);
 
 /* Self-test of the bounded waits of moe_matmul_fp8: a product of zeros (M, N, K up to

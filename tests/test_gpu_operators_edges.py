@@ -288,3 +288,40 @@ def test_matmul_waits_do_not_run_out_otherwise(torch, moe, M, N, K):
     from deterministic_expert_b200 import selftest_matmul_timeout
     assert selftest_matmul_timeout(M, N, K, K // 128) == moe.MOE_OK
     assert selftest_matmul_timeout(M, N, K, 1000) == moe.MOE_OK
+
+
+def test_matmul_errors_are_read_once_and_not_lost(torch, moe):
+    """Failing products on one stream while another thread reads the error word on its
+    own: each failure is seen by one of the two, and no more reads see one than waits
+    that could raise it."""
+    import threading
+    import time
+    from deterministic_expert_b200 import selftest_matmul_timeout
+    runs, seen, stop = 12, [0, 0], threading.Event()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    assert moe.operator_error() == moe.MOE_OK
+
+    def read():
+        while not stop.is_set():
+            status = moe.operator_error(stream=streams[1])
+            assert status in (moe.MOE_OK, moe.MOE_ETIMEOUT)
+            seen[1] += status == moe.MOE_ETIMEOUT
+
+    t = threading.Thread(target=read)
+    t.start()
+    try:
+        for _ in range(runs):
+            before = seen[1]
+            mine = selftest_matmul_timeout(100, 512, 2048, 3, stream=streams[0]) == moe.MOE_ETIMEOUT
+            seen[0] += mine
+            # What the self-test did not find, the other had taken: before it returned.
+            for _ in range(1000):
+                if mine or seen[1] > before:
+                    break
+                time.sleep(0.001)
+            assert mine or seen[1] > before
+    finally:
+        stop.set()
+        t.join()
+    assert sum(seen) >= runs
+    assert moe.operator_error() == moe.MOE_OK
