@@ -5,7 +5,10 @@ weighted combine with its gradient (include/moe.h documents the entry points).
 Like the rest of the binding these functions only check and marshal arguments.
 Outputs are allocated where they are not given; ``stream`` (default: the current
 stream of the tensors' device) is where the kernels run, and where outputs are
-allocated.  Tensors of a call live on one CUDA device, which need not be the
+allocated.  A stream that is given does not wait for the current one: the caller
+orders them (``wait_stream``) before the call, and before outputs are used elsewhere;
+the call's tensors may be dropped at once, their memory is kept until that stream is
+done with it.  Tensors of a call live on one CUDA device, which need not be the
 current one.
 """
 from __future__ import annotations
@@ -64,10 +67,18 @@ def _fn(name):
     return f
 
 
-def _call(name, device, stream, *args):
-    """Run an entry point with the tensors' device current, on `stream`."""
+def _call(name, device, stream, used, *args):
+    """Run an entry point with the tensors' device current, on `stream`; `used`: its
+    tensors (or None), which the allocator keeps for a stream that is not theirs."""
     f = _fns.get(name) or _fn(name)
-    s = _raw_stream(device.index) if stream is None else _handle(stream)
+    if stream is None:
+        s = _raw_stream(device.index)
+    else:
+        s = _handle(stream)
+        on = _moe._torch_stream(stream, device)
+        for t in used:
+            if t is not None:
+                t.record_stream(on)
     if device.index == torch.cuda.current_device():
         rc = f(*args, s)
     else:
@@ -160,7 +171,8 @@ def route(logits, k: int, *, scores: str = "softmax", bias=None, n_groups: int =
         out_w, = _empty(stream, dev, ((T, cfg.k), torch.float32))
     else:
         _tensor(out_w, "out_w", dev, _F32, (T, cfg.k))
-    _call("moe_route", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld,
+    _call("moe_route", dev, stream, (logits, bias, out_idx, out_w),
+          ctypes.byref(cfg), T, logits.data_ptr(), ld,
           None if bias is None else bias.data_ptr(), out_idx.data_ptr(), out_w.data_ptr())
     return out_idx, out_w
 
@@ -181,7 +193,8 @@ def route_backward(logits, idx, dw, *, scores: str = "softmax", n_groups: int = 
     if out is None:
         out, = _empty(stream, dev, ((T, E), logits.dtype))
     _tensor(out, "out", dev, (logits.dtype,), (T, E), contiguous=False)
-    _call("moe_route_backward", dev, stream, ctypes.byref(cfg), T, logits.data_ptr(), ld, idx.data_ptr(),
+    _call("moe_route_backward", dev, stream, (logits, idx, dw, out),
+          ctypes.byref(cfg), T, logits.data_ptr(), ld, idx.data_ptr(),
           dw.data_ptr(), out.data_ptr(), _rows(out, "out"))
     return out
 
@@ -201,7 +214,8 @@ def group_rows(idx, E: int, *, out=None, stream=None):
         _tensor(offsets, "offsets", dev, _I32, (int(E) + 1,))
         _tensor(token_of_row, "token_of_row", dev, _I32, (T * k,))
         _tensor(row_of_slot, "row_of_slot", dev, _I32, (T, k))
-    _call("moe_group_rows", dev, stream, T, k, int(E), idx.data_ptr(), offsets.data_ptr(), token_of_row.data_ptr(),
+    _call("moe_group_rows", dev, stream, (idx, offsets, token_of_row, row_of_slot),
+          T, k, int(E), idx.data_ptr(), offsets.data_ptr(), token_of_row.data_ptr(),
           row_of_slot.data_ptr())
     return offsets, token_of_row, row_of_slot
 
@@ -241,7 +255,8 @@ def quantize_rows_fp8(x, *, token_of_row=None, n_rows=None, out_codes=None, out_
         _tensor(token_of_row, "token_of_row", dev, _I32)
         R = int(token_of_row.shape[0])
     out_codes, out_scales, ld_s = _quant_out(R, K, out_codes, out_scales, dev, stream)
-    _call("moe_quantize_rows_fp8", dev, stream, R, K, x.data_ptr(), _DTYPES[x.dtype], ld, M,
+    _call("moe_quantize_rows_fp8", dev, stream, (x, token_of_row, n_rows, out_codes, out_scales),
+          R, K, x.data_ptr(), _DTYPES[x.dtype], ld, M,
           None if token_of_row is None else token_of_row.data_ptr(), _count(n_rows, dev), out_codes.data_ptr(),
           out_scales.data_ptr(), max(ld_s, R))
     return out_codes, out_scales
@@ -262,7 +277,8 @@ def quantize_weights_fp8(w, *, out_codes=None, out_scales=None, stream=None):
         out_scales, = _empty(stream, dev, (sshape, torch.float32))
     _tensor(out_codes, "out_codes", dev, _CODES, w.shape)
     _tensor(out_scales, "out_scales", dev, _F32, sshape)
-    _call("moe_quantize_weights_fp8", dev, stream, G, N, K, w.data_ptr(), out_codes.data_ptr(), out_scales.data_ptr())
+    _call("moe_quantize_weights_fp8", dev, stream, (w, out_codes, out_scales),
+          G, N, K, w.data_ptr(), out_codes.data_ptr(), out_scales.data_ptr())
     return out_codes, out_scales
 
 
@@ -291,7 +307,8 @@ def glu_quantize_fp8(gu, *, activation: int = 0, gate_clamp_max: float = float("
     dev = gu.device
     cfg = _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up)
     out_codes, out_scales, ld_s = _quant_out(R, I, out_codes, out_scales, dev, stream)
-    _call("moe_glu_quantize_fp8", dev, stream, ctypes.byref(cfg), R, I, gu.data_ptr(), ld, _count(n_rows, dev),
+    _call("moe_glu_quantize_fp8", dev, stream, (gu, n_rows, out_codes, out_scales),
+          ctypes.byref(cfg), R, I, gu.data_ptr(), ld, _count(n_rows, dev),
           out_codes.data_ptr(), out_scales.data_ptr(), max(ld_s, R))
     return out_codes, out_scales
 
@@ -306,7 +323,8 @@ def glu_backward_quantize_fp8(gu, dh, *, activation: int = 0, gate_clamp_max: fl
     _tensor(dh, "dh", dev, _BF16, (R, I), contiguous=False)
     cfg = _glu_config(activation, gate_clamp_max, up_clamp, situ_beta_gate, situ_beta_up)
     out_codes, out_scales, ld_s = _quant_out(R, 2 * I, out_codes, out_scales, dev, stream)
-    _call("moe_glu_backward_quantize_fp8", dev, stream, ctypes.byref(cfg), R, I, gu.data_ptr(), ld, dh.data_ptr(),
+    _call("moe_glu_backward_quantize_fp8", dev, stream, (gu, dh, n_rows, out_codes, out_scales),
+          ctypes.byref(cfg), R, I, gu.data_ptr(), ld, dh.data_ptr(),
           _rows(dh, "dh"), _count(n_rows, dev), out_codes.data_ptr(), out_scales.data_ptr(), max(ld_s, R))
     return out_codes, out_scales
 
@@ -338,7 +356,8 @@ def matmul_fp8(a, a_scale, w, w_scale, *, offsets=None, transposed: bool = False
         _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
         out, = _empty(stream, dev, ((M, width), out_dtype))
     _tensor(out, "out", dev, tuple(_DTYPES), (M, width), contiguous=False)
-    _call("moe_matmul_fp8", dev, stream, 1 if transposed else 0, G, None if offsets is None else offsets.data_ptr(),
+    _call("moe_matmul_fp8", dev, stream, (a, a_scale, w, w_scale, offsets, out),
+          1 if transposed else 0, G, None if offsets is None else offsets.data_ptr(),
           M, N, K, a.data_ptr(), a_scale.data_ptr(), max(ld_as, M), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
           _DTYPES[out.dtype], max(_rows(out, "out"), width))
     return out
@@ -367,7 +386,8 @@ def combine_rows(y, row_of_slot, w=None, *, addend=None, out=None, out_dtype=tor
         _need(out_dtype in _DTYPES, f"out_dtype: expected bfloat16 or float32, got {out_dtype}")
         out, = _empty(stream, dev, ((T, D), out_dtype))
     _tensor(out, "out", dev, tuple(_DTYPES), (T, D))
-    _call("moe_combine_rows", dev, stream, T, k, D, rows, y.data_ptr(), _DTYPES[y.dtype], max(ld, D),
+    _call("moe_combine_rows", dev, stream, (y, row_of_slot, w, addend, out),
+          T, k, D, rows, y.data_ptr(), _DTYPES[y.dtype], max(ld, D),
           row_of_slot.data_ptr(), None if w is None else w.data_ptr(),
           None if addend is None else addend.data_ptr(), out.data_ptr(), _DTYPES[out.dtype])
     return out
@@ -395,7 +415,8 @@ def combine_rows_backward(dout, y, row_of_slot, w=None, *, need_dw: bool = True,
     _need(rows <= 1 or _rows(out_dy, "out_dy") == ld, "out_dy: expected the row pitch of y")
     if need_dw:
         _tensor(out_dw, "out_dw", dev, _F32, (T, k))
-    _call("moe_combine_rows_backward", dev, stream, T, k, D, rows, dout.data_ptr(), y.data_ptr(), _DTYPES[y.dtype],
+    _call("moe_combine_rows_backward", dev, stream, (dout, y, row_of_slot, w, out_dy, out_dw if need_dw else None),
+          T, k, D, rows, dout.data_ptr(), y.data_ptr(), _DTYPES[y.dtype],
           max(ld, D), row_of_slot.data_ptr(), None if w is None else w.data_ptr(), out_dy.data_ptr(),
           out_dw.data_ptr() if need_dw else None)
     return out_dy, (out_dw if need_dw else None)

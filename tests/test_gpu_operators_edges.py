@@ -325,3 +325,54 @@ def test_matmul_errors_are_read_once_and_not_lost(torch, moe):
         t.join()
     assert sum(seen) >= runs
     assert moe.operator_error() == moe.MOE_OK
+
+
+# ------------------------------------------------------------ given streams
+def _calls(torch, moe):
+    """Every operator with tensors of its own: (call of (tensors, stream), tensors)."""
+    g = torch.Generator().manual_seed(3)
+
+    def rn(*shape, dtype=torch.float32):
+        return torch.randn(*shape, generator=g).to(dtype).cuda()
+
+    bf = torch.bfloat16
+    x, logits, bias = rn(64, 512, dtype=bf), rn(64, 16), rn(16)
+    idx, w = moe.route(logits, 4)
+    off, tok, slot = moe.group_rows(idx, 16)
+    q, s = moe.quantize_rows_fp8(x, token_of_row=tok)
+    wq, ws = moe.quantize_weights_fp8(rn(16, 256, 512, dtype=bf))
+    y, gu, dh, n = rn(256, 512, dtype=bf), rn(256, 512, dtype=bf), rn(256, 256, dtype=bf), off[16:].clone()
+    return {
+        "route": (lambda t, st: moe.route(t[0], 4, bias=t[1], stream=st), (logits, bias)),
+        "route_backward": (lambda t, st: moe.route_backward(t[0], t[1], t[2], stream=st), (logits, idx, w)),
+        "group_rows": (lambda t, st: moe.group_rows(t[0], 16, stream=st), (idx,)),
+        "quantize_rows_fp8": (lambda t, st: moe.quantize_rows_fp8(t[0], token_of_row=t[1], n_rows=t[2], stream=st), (x, tok, n)),
+        "quantize_weights_fp8": (lambda t, st: moe.quantize_weights_fp8(t[0], stream=st), (y,)),
+        "glu_quantize_fp8": (lambda t, st: moe.glu_quantize_fp8(t[0], stream=st), (gu,)),
+        "glu_backward_quantize_fp8": (lambda t, st: moe.glu_backward_quantize_fp8(t[0], t[1], stream=st), (gu, dh)),
+        "matmul_fp8": (lambda t, st: moe.matmul_fp8(*t[:4], offsets=t[4], stream=st), (q, s, wq, ws, off)),
+        "combine_rows": (lambda t, st: moe.combine_rows(t[0], t[1], t[2], addend=t[3], stream=st), (y, slot, w, x)),
+        "combine_rows_backward": (lambda t, st: moe.combine_rows_backward(t[3], t[0], t[1], t[2], stream=st), (y, slot, w, x)),
+    }
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_tensors_dropped_after_a_call_on_another_stream(torch, moe, raw):
+    """A busy stream reads its tensors long after the caller let go of them: their
+    memory is not handed out meanwhile."""
+    side = torch.cuda.Stream()
+    for name, (call, tensors) in _calls(torch, moe).items():
+        want = call(tensors, None)
+        torch.cuda.synchronize()
+        mine = [t.clone() for t in tensors]
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)       # about 10 ms
+        got = call(mine, side.cuda_stream if raw else side)
+        del mine
+        # The same sizes again, which the allocator would take from what was dropped.
+        other = [torch.zeros_like(t) for t in tensors for _ in range(2)]
+        torch.cuda.synchronize()
+        for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
+        del other
