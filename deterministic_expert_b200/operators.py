@@ -10,6 +10,11 @@ orders them (``wait_stream``) before the call, and before outputs are used elsew
 the call's tensors may be dropped at once, their memory is kept until that stream is
 done with it.  Tensors of a call live on one CUDA device, which need not be the
 current one.
+
+Autograd does not see these calls: gradients are operators of their own
+(``route_backward``, ``combine_rows_backward``, ...).  A tensor that requires a
+gradient is refused while gradients are recorded; pass it detached, or call under
+``torch.no_grad()`` or in an ``autograd.Function``.
 """
 from __future__ import annotations
 
@@ -54,6 +59,7 @@ ARGTYPES = {
 }
 _fns: dict = {}
 _Tensor = torch.Tensor
+_grad_enabled = torch.is_grad_enabled
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -108,9 +114,12 @@ def _need(cond, what):
 def _tensor(t, name, device, dtypes, shape=None, contiguous=True):
     """Refuse a tensor the library would read or write wrongly."""
     if (isinstance(t, _Tensor) and t.is_cuda and (device is None or t.device == device) and t.dtype in dtypes
-            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())
+            and not (t.requires_grad and _grad_enabled())):
         return
     _need(isinstance(t, _Tensor), f"{name}: expected a tensor")
+    _need(not (t.requires_grad and _grad_enabled()),
+          f"{name}: requires a gradient, which this call would not record: detach it, or call under torch.no_grad()")
     _need(t.is_cuda and (device is None or t.device == device),
           f"{name}: expected a CUDA tensor" + (f" on {device}, got {t.device}" if device is not None else ""))
     _need(t.dtype in dtypes, f"{name}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")

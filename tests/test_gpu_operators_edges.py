@@ -376,3 +376,37 @@ def test_tensors_dropped_after_a_call_on_another_stream(torch, moe, raw):
         for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
         del other
+
+
+def test_tensors_that_require_a_gradient(torch, moe):
+    """Refused where a gradient would be lost, each tensor of each call; taken without
+    one, and inside an autograd function."""
+    for name, (call, tensors) in _calls(torch, moe).items():
+        for i, t in enumerate(tensors):
+            if not t.is_floating_point():
+                continue
+            mine = list(tensors)
+            mine[i] = t.clone().requires_grad_()
+            with pytest.raises(ValueError, match="gradient"):
+                call(mine, None)
+            with torch.no_grad():
+                call(mine, None)
+
+    class Weights(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits):
+            idx, w = moe.route(logits, 4, renormalize=True)
+            ctx.save_for_backward(logits, idx)
+            ctx.mark_non_differentiable(idx)
+            return idx, w
+
+        @staticmethod
+        def backward(ctx, _, dw):
+            logits, idx = ctx.saved_tensors
+            return moe.route_backward(logits, idx, dw.contiguous(), renormalize=True)
+
+    l = torch.randn(8, 16, generator=torch.Generator().manual_seed(1)).cuda().requires_grad_()
+    dw = torch.randn(8, 4, generator=torch.Generator().manual_seed(2)).cuda()
+    idx, w = Weights.apply(l)
+    w.backward(dw)
+    assert torch.equal(l.grad, moe.route_backward(l.detach(), idx, dw, renormalize=True))

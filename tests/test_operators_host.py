@@ -186,6 +186,25 @@ def test_binding_refuses_host_tensors():
             call()
 
 
+def test_binding_refuses_tensors_whose_gradient_it_would_drop():
+    x = torch.zeros(4, 128, dtype=torch.bfloat16)
+    i = torch.zeros(4, 2, dtype=torch.int32)
+    c = torch.zeros(4, 128, dtype=torch.uint8)
+    s, g = torch.zeros(1, 4), torch.zeros(4, 2)
+    xg, sg, gg = (t.clone().requires_grad_() for t in (x, s, g))
+    calls = (lambda x, s, g: moe.route(x, 2), lambda x, s, g: moe.route_backward(x, i, g),
+             lambda x, s, g: moe.quantize_rows_fp8(x), lambda x, s, g: moe.quantize_weights_fp8(x),
+             lambda x, s, g: moe.glu_quantize_fp8(x), lambda x, s, g: moe.glu_backward_quantize_fp8(x, x),
+             lambda x, s, g: moe.combine_rows(x, i, g), lambda x, s, g: moe.combine_rows_backward(x, x, i, g))
+    for n, call in enumerate(calls):
+        with pytest.raises(ValueError, match="gradient"):
+            call(xg, sg, gg)
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):      # refused as host tensors only
+            call(xg, sg, gg)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(xg.detach(), sg.detach(), gg.detach())
+
+
 def test_operators_are_reached_through_the_package():
     for n in moe.OPERATORS:
         assert callable(getattr(moe, n))
