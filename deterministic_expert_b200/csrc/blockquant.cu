@@ -30,7 +30,6 @@ constexpr float kE4m3Max = 448.f;
 // ulp, each product rounds by half of one: 2^-20 covers all of it four times).
 struct BlockScale {
   float s, inv, lo, hi;
-  float size, unit;   // 2^e and s / 2^e (2^e <= s)
   float rem;   // amax - 448 s, exact (0 for a raised scale, whose division is by a power of two)
 };
 
@@ -51,9 +50,6 @@ __device__ __forceinline__ BlockScale block_scale(float amax) {
     b.s = __int_as_float(0x7fffffff);
     b.inv = 0.f;
   }
-  const uint32_t e = __float_as_uint(b.s) & 0x7f800000u;
-  b.size = __uint_as_float(e);
-  b.unit = b.s * __uint_as_float(0x7f000000u - e);
   b.lo = b.inv * (1.f - 0x1p-20f);
   b.hi = b.inv * (1.f + 0x1p-20f);
   return b;
@@ -108,9 +104,11 @@ __device__ __forceinline__ uint32_t e4m3x2(uint64_t p) {
 // of its size away.  So x / s lies beside a middle only where 448 x / amax is one,
 // and then on the side that the rounding of s to fp32 went away from: a
 // reciprocal 2^-18 too small (s rounded up) or too large (down) takes every such
-// element to its side and no other across.  Where s = amax / 448 exactly, the
-// quotient is corrected by its exact remainder, so that middles are met exactly and
-// go to the even code.
+// element to its side and no other across.  Where s = amax / 448 exactly, it is a
+// number of at most 6 bits times a power of two: the quotient, known to 2^-21, is a
+// middle or at least 2^-10.2 of its size away from one, so that rounding it to 16 bits
+// meets middles exactly, which go to the even code, and takes no other across.  (An
+// exact remainder x - q s instead would underflow for tiny s.)
 __device__ __forceinline__ uint2 codes8_bf16(const float (&v)[8], const BlockScale& b) {
   const float f = b.rem == 0.f ? b.inv : b.inv * (b.rem < 0.f ? 1.f - 0x1p-18f : 1.f + 0x1p-18f);
   const uint64_t f2 = pair(f, f);
@@ -121,13 +119,13 @@ __device__ __forceinline__ uint2 codes8_bf16(const float (&v)[8], const BlockSca
     q[i] = mul2(x[i], f2);
   }
   if (b.rem == 0.f) {
-    // q - (q s - x) f: with a zero remainder (always +0) a zero keeps its sign.  The
-    // remainder is about x 2^-24, which would underflow for small s, so that it is
-    // formed of x and s divided by 2^e.
-    const float up = __uint_as_float(0x7f000000u - __float_as_uint(b.size)), down = f * b.size;
-    const uint64_t s2 = pair(b.unit, b.unit), one = pair(-up, -up), n2 = pair(-down, -down);
+    // Veltkamp's split: t - (t - q) with t = 257 q.
+    const uint64_t up = pair(257.f, 257.f), one = pair(-1.f, -1.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = fma2(fma2(q[i], s2, mul2(x[i], one)), n2, q[i]);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t t = mul2(q[i], up);
+      q[i] = fma2(fma2(q[i], one, t), one, t);
+    }
   }
   const uint2 c = make_uint2(e4m3x2(q[0]) | e4m3x2(q[1]) << 16, e4m3x2(q[2]) | e4m3x2(q[3]) << 16);
   return c;
@@ -243,7 +241,7 @@ __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantA
     }
     const float sg = sigmoid_f32<GLU == kSwigluClamped>(g, c);
     if (GRAD) {
-      // d sigmoid(g) is a factor of both (24576 x 1408: 60.4 us; each on its own 66).
+      // d sigmoid(g) is a factor of both (24576 x 1408, caches cold: 60.4 us; each on its own 66).
       const float ds = d * sg;
       first = ds * bv * fmaf(g, c, 1.f);
       second = ds * g;
@@ -263,15 +261,17 @@ __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantA
 // threads takes 32 rows (their scales of a block are one 128-byte segment) and
 // walks their blocks, U at a time so that their loads are in flight together.
 // Bound by memory: every element is read once and its code written once.  24576 bf16
-// rows of 2048: 26.2 us (5.8 TB/s; with three resident CTAs, where the compiler would
-// take 67 registers, 27.8), and 22.7 us a call gathered from 4096 rows, which then come through L2.  Gated unit of 32768 x 2048: 61 us
-// (5.5 TB/s); its gradient, 24576 x 1408: 55 us (5.0 TB/s).
+// rows of 2048: 25.7 us (6.0 TB/s; two blocks at a time 27.3), and 21.1 us gathered from
+// 4096 rows, which then come through L2.  fp32 rows 45.7 us (5.5 TB/s).  Gated unit of
+// 32768 x 2048: 58.5 us (5.8 TB/s), clamped 79, SiTU 185 (two tanhf and two divisions
+// an element); its gradient, 24576 x 1408: 54-57 us (4.9-5.2 TB/s), clamped 81, SiTU
+// 133.
 constexpr int kRowsPerCta = 32;
 template <int KIND>
 constexpr int kUnroll = KIND == kQuantBf16 ? 4 : 1;
 
 template <int KIND, int GLU = kSwiglu>
-__global__ void __launch_bounds__(256, KIND == kQuantBf16 ? 4 : 1) k_quant_blocks(const QuantArgs a) {
+__global__ void __launch_bounds__(256) k_quant_blocks(const QuantArgs a) {
   constexpr int U = kUnroll<KIND>;
   constexpr bool GRAD = KIND == kQuantGluBackward;
   griddep_wait();
@@ -373,7 +373,8 @@ __global__ void __launch_bounds__(256, KIND == kQuantBf16 ? 4 : 1) k_quant_block
 }
 
 // One CTA per 128 x 128 block of one group's weights: every thread holds 64
-// elements, so the block is read once.
+// elements, so the block is read once.  Bound by memory: 8 x 4096 x 7168 in 102 us
+// (6.9 TB/s).
 __global__ void __launch_bounds__(256) k_quant_weights_block(const uint16_t* w, uint8_t* codes,
                                                              float* scales, int N, int K) {
   griddep_wait();

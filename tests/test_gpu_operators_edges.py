@@ -261,6 +261,21 @@ def test_quantize_tiny_blocks_bf16(torch, moe):
         assert np.array_equal(w.cpu().numpy(), rq[r:r + 1]) and float(ws[0, 0]) == float(rs[0, r])
 
 
+def test_quantize_every_bf16_significand(torch, moe):
+    """Every pair of significands of an element and its block's maximum, over the
+    binades that codes reach."""
+    rows = []
+    for b in range(128, 256):
+        x = np.array([a * 2.0 ** e for e in range(-18, 1) for a in range(128, 256)])
+        x = x[x <= b]
+        for i in range(0, len(x), 127):
+            rows.append(np.concatenate([[b], np.resize(x[i:i + 127], 127)]))
+    x = np.array(rows) * np.resize([1.0, -1.0], len(rows))[:, None]
+    q, s = moe.quantize_rows_fp8(torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16).cuda())
+    rq, rs = R.quantize_rows(x)
+    assert np.array_equal(s.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+
+
 # ---------------------------------------------------------------- time-outs
 @pytest.mark.parametrize("M,N,K,loaded", [(8, 128, 4096, 0), (8, 128, 4096, 3), (20, 300, 8192, 1), (100, 512, 2048, 6),
                                           (600, 512, 8192, 0), (2560, 2048, 2048, 0), (2560, 2048, 2048, 9),
