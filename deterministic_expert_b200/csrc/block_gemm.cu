@@ -18,8 +18,8 @@
 // P_b back takes another 512 (128 KB at TMEM's rate) plus the latencies of commit,
 // first load and release; the two accumulator buffers of 256 TMEM columns overlap the
 // two, and the round trip of a buffer through both, about 880 cycles a block, is what
-// bounds large products: 8192 x 4096 x 7168 in 219 us, 2190 TFLOP/s, the tensor pipe
-// busy half of the time.  A tile's store costs 1.3 us (all SMs write at once) and its
+// bounds large products: 8192 x 4096 x 7168 in 212-217 us, 2220-2270 TFLOP/s, the
+// tensor pipe busy half of the time.  A tile's store costs 1.3 us (all SMs write at once) and its
 // start 0.5 us, which short contractions feel.  Few rows a group are bound by the
 // weights' stream: 384 rows over 64 groups of 2816 x 2048 at 5.9-6.1 TB/s.
 //

@@ -250,7 +250,7 @@ __device__ __noinline__ int select_exact(const RouteOpArgs& a, const In* row, in
 // winner moves up its list; lane j notes the key and the winner of slot j and looks
 // its expert up among the winner's keys when all are known.
 // Bound by instructions issued: T = 8192, E = 256, k = 8 in 8 groups reads 8.4 MB fp32
-// (1.3 us of memory) and takes 13.3 us, one token 4.3.  A lane's whole sort network
+// (1.3 us of memory) and takes 13.8 us, one token 4.1.  A lane's whole sort network
 // is cheaper than searching its keys in every round; a row that has to be decided
 // in fp64 costs the launch up to 8 us.
 // The resident CTAs keep the fp64 pass, which few rows take, from costing the others
@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(256, CPL == 4 ? 5 : CPL <= 8 ? 4 : CPL <= 16 ?
 // The row is written once (zeros, or the softmax's common term); the chosen
 // experts' lanes then write theirs.
 // Bound by memory: every logit of the row is written, and read for a plain
-// softmax (T = 16384, E = 128 fp32: 17.8 MB, 8.3 us, 2.1 TB/s: the row is in the
-// caches by the time the chosen lanes' part is known).
+// softmax (T = 16384, E = 128 fp32: 17.8 MB, 6.2 us with the rows in L2, 12.7 without).
+// The row is in the caches by the time the chosen lanes' part is known.
 template <int PER, int VEC, typename In>
 __global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
   griddep_wait();
@@ -599,8 +599,8 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
 // with one expert come from a vote on each of its bits: match.any costs the SM
 // about 40 cycles a time).  Integers only, the order is the
 // list's: stable by token, then slot.  No workspace and one launch, whatever T.
-// Bound by latency: the list is small (T = 8192, k = 8, E = 256: 262 KB in 12.4 us;
-// one token 6.8 us, most of it the two cluster barriers and the prefix over warps).
+// Bound by latency: the list is small (T = 8192, k = 8, E = 256: 262 KB in 12.1 us;
+// one token 6.5 us, most of it the two cluster barriers and the prefix over warps).
 constexpr int kGroupCtas = 8;
 constexpr int kGroupThreads = 1024;
 constexpr int kAtOnce = 8;

@@ -8,7 +8,7 @@ stream of the tensors' device) is where the kernels run, and where outputs are
 allocated.  A stream that is given does not wait for the current one: the caller
 orders them (``wait_stream``) before the call, and before outputs are used elsewhere;
 the call's tensors may be dropped at once, their memory is kept until that stream is
-done with it.  Tensors of a call live on one CUDA device, which need not be the
+done with it (a stream given by its raw handle has to outlive them).  Tensors of a call live on one CUDA device, which need not be the
 current one.
 
 Autograd does not see these calls: gradients are operators of their own

@@ -568,8 +568,9 @@ typedef struct moe_route_config {
  * (bias [E] fp32 or NULL; it selects only).  With topk_groups < n_groups the
  * best topk_groups groups stay; of their experts the k with the largest keys are
  * chosen, in descending order; equal keys or group scores go to the lower index.
- * Without a bias the order is that of exact arithmetic (scores that round to 1 or 0
- * are told apart by their logits); with one that of 64-bit keys.  Weights are
+ * Without a bias experts are ordered by their logits, and groups by sums of scores
+ * known to 2^-48 of themselves, or of their distance from 1 or 2 (scores that round to
+ * 1 or 0 are told apart); with one the order is that of 64-bit keys.  Weights are
  * scores (over their sum if renormalize) times routed_scale, fp32.
  * An expert whose logit or key is -inf or NaN is never chosen (nor counted in
  * the softmax); slots without an expert get index -1 and weight 0, so a padding
