@@ -197,6 +197,9 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&v)[8]) {
 // added to the tail.  ex2 4 2^-24, the correction, its product and 1 + e one each at
 // most, rcp 2.  Below -87.3 the result is 0.  c: 1 - sigmoid(g) = e^-g sigmoid(g), as
 // accurate (1 where e^-g is infinite: the product with 0 is a NaN, which fminf drops).
+// From kSure on s is 1; units that are finite for an infinite gate, or whose lost part
+// would be infinite, bound the gate by it.
+constexpr float kSure = 128.f;
 template <bool ANY>
 __device__ __forceinline__ float sigmoid_f32(float g, float& c) {
   constexpr float kHead = 47274.f / 32768.f, kTail = 4.88849515e-6f;   // tail: 1 - head ln 2
@@ -221,7 +224,7 @@ template <int GLU, bool GRAD>
 __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantArgs& a, float& first, float& second) {
   float c;
   if (GLU == kSitu) {
-    const float sg = sigmoid_f32<false>(g, c);
+    const float sg = sigmoid_f32<false>(fminf(g, kSure), c);
     const float tg = tanhf(__fdiv_rn(g, a.beta_g)), tu = tanhf(__fdiv_rn(u, a.beta_u));
     const float av = a.beta_g * tg * sg, bv = a.beta_u * tu;
     if (GRAD) {
@@ -239,7 +242,7 @@ __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantA
       upass = (u > a.up_clamp || u < -a.up_clamp) ? 0.f : 1.f;
       bv = u > a.up_clamp ? a.up_clamp : (u < -a.up_clamp ? -a.up_clamp : u);
     }
-    const float sg = sigmoid_f32<GLU == kSwigluClamped>(g, c);
+    const float sg = GLU == kSwigluClamped ? sigmoid_f32<true>(fminf(g, kSure), c) : sigmoid_f32<false>(g, c);
     if (GRAD) {
       // d sigmoid(g) is a factor of both (24576 x 1408, caches cold: 60.4 us; each on its own 66).
       const float ds = d * sg;
@@ -263,8 +266,8 @@ __device__ __forceinline__ void glu_unit(float g, float u, float d, const QuantA
 // Bound by memory: every element is read once and its code written once.  24576 bf16
 // rows of 2048: 25.7 us (6.0 TB/s; two blocks at a time 27.3), and 21.1 us gathered from
 // 4096 rows, which then come through L2.  fp32 rows 45.7 us (5.5 TB/s).  Gated unit of
-// 32768 x 2048: 58.5 us (5.8 TB/s), clamped 79, SiTU 185 (two tanhf and two divisions
-// an element); its gradient, 24576 x 1408: 54-57 us (4.9-5.2 TB/s), clamped 81, SiTU
+// 32768 x 2048: 58.5 us (5.8 TB/s), clamped 80, SiTU 187 (two tanhf and two divisions
+// an element); its gradient, 24576 x 1408: 54-57 us (4.9-5.2 TB/s), clamped 83, SiTU
 // 133.
 constexpr int kRowsPerCta = 32;
 template <int KIND>

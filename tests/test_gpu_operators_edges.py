@@ -117,6 +117,30 @@ def test_glu_situ_gradient_is_accurate(torch, moe):
     assert np.all(np.abs(got - np.abs(slope * R.sigmoid(g) + t2) * b) <= 40 * U * (R.sigmoid(g) + np.abs(t2)) * b)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(up_clamp=2.0), dict(gate_clamp_max=3.3e38), dict(activation=1)], ids=str)
+def test_glu_of_the_largest_gates(torch, moe, kw):
+    """Gates whose product with log2 e is past fp32: the sigmoid is 1 or 0, the unit and
+    its gradient are finite; infinities and NaN give the block's scale NaN."""
+    big = [2.3e38, 2.4e38, 3.3e38, -2.3e38, -2.4e38, -3.3e38]
+    gu = torch.cat([_one_a_block(torch, big, 128), _one_a_block(torch, [0.5] * 6, 128)], dim=1)
+    one = _one_a_block(torch, [1.0] * 6, 128)
+    ref = dict(act="situ") if kw.get("activation") else dict(cg=kw.get("gate_clamp_max", np.inf), cu=kw.get("up_clamp", np.inf))
+    for (q, s), want in ((moe.glu_quantize_fp8(gu, **kw), R.glu(gu.double().cpu().numpy(), **ref)),
+                         (moe.glu_backward_quantize_fp8(gu, one, **kw),
+                          R.glu_backward(gu.double().cpu().numpy(), one.double().cpu().numpy(), **ref))):
+        for b in range(s.shape[0]):
+            w = np.abs(want[:, b * 128])
+            got = np.where(w == 0, 0.0, _values(s)[b])
+            assert np.all(np.abs(got - w) <= 40 * U * np.maximum(w, 1e-30)), (b, got, w)
+            assert np.all((q.cpu().numpy()[:, b * 128] & 0x7F) == np.where(w == 0, 0, 0x7E))
+    for v in (float("inf"), float("nan")):
+        bad = gu.clone()
+        bad[0, 0] = v
+        _, s = moe.glu_quantize_fp8(bad, **kw)
+        clamped = v > 0 and (kw.get("gate_clamp_max") or kw.get("activation"))
+        assert torch.isnan(s[0, 0]).item() == (not clamped) and not torch.isnan(s[0, 1:]).any()
+
+
 # ----------------------------------------------------------------- routing
 def _exact_route(l, k, scores, n_groups, keep):
     """Experts of one row without a bias, groups scored by their two best, in decimals
@@ -391,6 +415,27 @@ def test_tensors_dropped_after_a_call_on_another_stream(torch, moe, raw):
         for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), name
         del other
+
+
+def test_captured_on_a_given_stream(torch, moe):
+    """A graph of calls on a given stream whose temporaries are dropped meanwhile."""
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn(64, 512, generator=g).to(torch.bfloat16).cuda()
+    w, sw = moe.quantize_weights_fp8(torch.randn(256, 512, generator=g).to(torch.bfloat16).cuda())
+    want = moe.matmul_fp8(*moe.quantize_rows_fp8(x), w, sw)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for _ in range(3):
+            q, s = moe.quantize_rows_fp8(x, stream=side)
+            out = moe.matmul_fp8(q, s, w, sw, stream=side.cuda_stream)
+            del q, s
+    out.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
 
 
 def test_tensors_that_require_a_gradient(torch, moe):
