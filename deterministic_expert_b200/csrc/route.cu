@@ -504,8 +504,10 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackArgs a) {
     if (e < 0 || e >= a.E) { e = -1; dw = 0.f; }
   }
   const float lj = e >= 0 ? to_float(row[e]) : -INFINITY;
-  // -inf and NaN logits are never chosen; an index given for one gets no gradient.
+  // -inf and NaN logits are never chosen; an index given for one gets no gradient, and
+  // its dw, whatever it is, is in no sum.
   const bool have = lj > -INFINITY;
+  if (!have) dw = 0.f;
 
   auto store = [](float v) {
     if constexpr (sizeof(In) == 2) return static_cast<In>(pack_bf16x2(v, 0.f) & 0xFFFFu);

@@ -240,6 +240,25 @@ def test_route_group_sums_past_fp32(torch, moe):
     assert want.tolist() == [[2, 3]] and idx.cpu().numpy().tolist() == want.tolist()
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_backward_of_masked_logits(torch, moe, scores, renorm):
+    """An index given for a masked logit has no gradient, whatever its dw is."""
+    g = torch.Generator().manual_seed(4)
+    l, dw = torch.randn(6, 24, generator=g), torch.randn(6, 3, generator=g)
+    idx = torch.tensor([[0, 5, 9]] * 6, dtype=torch.int32)
+    l[0, 5], l[1, 5], l[2, 0] = float("-inf"), float("nan"), float("-inf")
+    dw[0, 1], dw[1, 1], dw[2, 0] = float("inf"), 1.0, float("nan")
+    idx[3, 1], dw[3, 1] = -1, float("nan")
+    idx[4, 2], dw[4, 2] = 24, float("inf")
+    got = moe.route_backward(l.cuda(), idx.cuda(), dw.cuda(), scores=scores, renormalize=renorm).cpu()
+    clean = dw.clone()
+    for t, j in ((0, 1), (1, 1), (2, 0), (3, 1), (4, 2)):
+        clean[t, j] = 0.0
+    want = R.route_backward(l.double().numpy(), idx.numpy(), clean.double().numpy(), scores, renorm)
+    assert np.all(np.abs(got.double().numpy() - want) <= 1e-6)      # |dw| sums to less than 6; 64 U each
+
+
 # ------------------------------------------------------------ quantisation
 def _tiny_blocks(exact_in):
     """Blocks whose scale is exact (or raised to 2^-126), filled with exact middles of
